@@ -38,12 +38,14 @@
 extern "C" {
 #endif
 
-/* Storage / arithmetic type of muon_ns_orthogonalize's matrices. */
+/* Storage / arithmetic type of muon_ns_orthogonalize's matrices (MUON_BF16 or
+ * MUON_FP32), and of the layer operators' matrices (any of the three). */
 typedef enum {
   MUON_BF16 = 0, /* bf16 storage; bf16 tensor-core operands, fp32 accumulate,
                     X kept between steps as the pair bf16 hi + int8 residual
                     (see muon_bx_bf16), about 16 significant bits */
-  MUON_FP32 = 1  /* fp32 storage; fp32 SIMT FMA verification path */
+  MUON_FP32 = 1, /* fp32 storage; fp32 SIMT FMA verification path */
+  MUON_FP16 = 2  /* the layer operators only (muon_layer_norm ... muon_mx_product) */
 } muon_dtype;
 
 typedef enum {
@@ -330,6 +332,111 @@ int muon_bx_apply_bf16(int batch, int m, int n, int ldx, const void* B, int ldb,
                        void* stream);
 
 /*
+ * The layer operators: what runs around the weights that muon_step updates.
+ *
+ * They follow the conventions above, except that their matrices may have a row
+ * stride (ld, in elements, >= cols; not looked at for one row), need only the
+ * alignment of their element type, and may have up to 2^30 rows and columns,
+ * zero rows among them.  An output matrix must not overlap an input, counted
+ * from its first to its last element (MUON_ERR_ARG).  They take no workspace
+ * and can be captured into a CUDA graph from their first call on a stream;
+ * what a captured call bakes in is the caller's own pointers.  dtype is a
+ * muon_dtype.
+ */
+
+/*
+ * muon_layer_norm -- y = (x - mean) * rstd * weight + bias for every row.
+ *
+ * mean and rstd = 1 / sqrt(mean((x - mean)^2) + eps) are fp32 sums in a fixed
+ * order, the variance over centred values; y is rounded once.
+ * rows, cols   rows >= 0, cols >= 1.
+ * x, ldx       input, dtype; y, ldy: output, dtype.
+ * weight, bias cols values of param_dtype (MUON_FP32 or dtype), or NULL for 1
+ *              and 0.
+ * mean, rstd   rows fp32 values each, written (the backward pass takes them).
+ */
+int muon_layer_norm(long long rows, long long cols, const void* x, long long ldx, int dtype, const void* weight,
+                    const void* bias, int param_dtype, float eps, void* y, long long ldy, float* mean, float* rstd,
+                    void* stream);
+
+/*
+ * muon_layer_norm_backward -- gradients of muon_layer_norm.
+ *
+ * With xhat = (x - mean) * rstd and g = dy * weight:
+ *   dx      = rstd * (g - mean(g) - xhat * mean(g * xhat))    (per row, dtype)
+ *   dweight = sum over rows of dy * xhat,  dbias = sum over rows of dy
+ * dweight, dbias: cols values of param_dtype, written; NULL where not wanted
+ *   (zeros for no rows).  The sums are fp32 in a fixed order.
+ * mean, rstd: as muon_layer_norm wrote them.  weight: NULL for 1.
+ * scratch: DEVICE memory, 16-byte aligned, of at least
+ *   muon_layer_norm_scratch_bytes(rows, cols) bytes, the call's own until it
+ *   has run; unused (may be NULL) when neither dweight nor dbias is wanted.
+ */
+int muon_layer_norm_backward(long long rows, long long cols, const void* dy, long long lddy, const void* x, long long ldx,
+                             int dtype, const void* weight, int param_dtype, const float* mean, const float* rstd, void* dx,
+                             long long lddx, void* dweight, void* dbias, void* scratch, long long scratch_bytes,
+                             void* stream);
+
+/* Bytes of scratch of a backward pass on the current device; `bytes` is a HOST pointer. */
+int muon_layer_norm_scratch_bytes(long long rows, long long cols, long long* bytes);
+
+/*
+ * 4-bit microscaled (MX) matrices: E2M1 values (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives) in blocks of 32 along each row, with one power-of-two scale
+ * a block.  A matrix of rows x cols is held as
+ *   data    rows of 16 * ceil(cols / 32) bytes, two values a byte, the even
+ *           column in the low half; code = 8 * sign + index of the magnitude;
+ *   scales  ceil(rows / 128) x ceil(cols / 128) tiles of 512 bytes: block
+ *           4 C + b of row 128 R + 32 j + r (r < 32) has byte
+ *           512 * (R * ceil(cols / 128) + C) + 16 r + 4 j + b,
+ *           and stands for 2^(byte - 127); 255 is a NaN;
+ * both 16-byte aligned, with zeros in the places beyond the matrix (the data
+ * of the last block of each row, the rest of each scale tile).
+ *
+ * muon_mx_quantize -- matrices to their 4-bit form, `count` of them in one call.
+ *
+ * Per block: byte = max(0, E - 2), E the biased fp32 exponent of the largest
+ * magnitude (255 when the block holds an infinity or a NaN, so that every
+ * value of it, and every sum that takes one, is NaN); each value divided by
+ * the scale is rounded to the nearest code, ties to the even one, and held at
+ * 6 (OCP Microscaling Formats v1.0).
+ * x        HOST array of `count` DEVICE pointers, dtype; shapes: HOST array of
+ *          2 * count int64, rows and cols; strides: HOST array of row strides
+ *          in elements, or NULL for contiguous rows.
+ * row_data, row_scales   HOST arrays of DEVICE pointers to the form with blocks
+ *          along the rows, or both NULL.
+ * col_data, col_scales   the form with blocks along the columns: that of the
+ *          transpose, cols x rows; or both NULL.  Both forms come from one read.
+ * Matrices with no rows or no columns are left out.
+ */
+int muon_mx_quantize(int count, const void* const* x, const int64_t* shapes, const int64_t* strides, int dtype,
+                     void* const* row_data, void* const* row_scales, void* const* col_data, void* const* col_scales,
+                     void* stream);
+
+/*
+ * muon_mx_dequantize -- the values that 4-bit matrices stand for, y contiguous
+ * rows x cols of dtype.  Exact in MUON_BF16 and MUON_FP32; rounded to nearest
+ * in MUON_FP16 (beyond its range to an infinity or 0).
+ */
+int muon_mx_dequantize(int count, const void* const* data, const void* const* scales, const int64_t* shapes,
+                       void* const* y, int dtype, void* stream);
+
+/*
+ * muon_mx_product -- out = A B^T of 4-bit matrices A (m x k) and B (n x k), on
+ * the tensor cores, summed in fp32 in a fixed order and rounded once to out
+ * (m x n, row stride ldo, dtype).  k == 0 writes zeros.
+ * The three products of a linear layer y = x W^T:
+ *   y  = A = rows of x,    B = rows of W
+ *   dx = A = rows of dy,   B = columns of W
+ *   dW = A = columns of dy, B = columns of x
+ * A wait that runs out is recorded as for the other tensor-core calls; of a
+ * captured call on a stream that had no status word, in one word a device,
+ * which muon_get_status of any stream of it reports.
+ */
+int muon_mx_product(long long m, long long n, long long k, const void* a_data, const void* a_scales, const void* b_data,
+                    const void* b_scales, void* out, long long ldo, int dtype, void* stream);
+
+/*
  * muon_get_status -- synchronise `stream`, then return and clear the device
  * status word of (current device, stream): MUON_OK or MUON_ERR_DEVICE_TIMEOUT,
  * or MUON_ERR_CUDA if the synchronisation itself failed.
@@ -397,7 +504,12 @@ typedef enum {
   MUON_KERNEL_SCALE = 9, /* per-matrix 1 / (||u||_F + eps) */
   MUON_KERNEL_BX_APPLY = 10, /* tensor cores: the last step's X' = aX + BX applied to W */
   MUON_KERNEL_NORM = 11,     /* per-neuron rescale: row norms, state, factors */
-  MUON_KERNEL_KINDS = 12
+  MUON_KERNEL_LAYER_NORM = 12,
+  MUON_KERNEL_LAYER_NORM_GRAD = 13,
+  MUON_KERNEL_MX_QUANTIZE = 14,
+  MUON_KERNEL_MX_DEQUANTIZE = 15,
+  MUON_KERNEL_MX_PRODUCT = 16, /* tensor cores: C = A B^T of 4-bit matrices */
+  MUON_KERNEL_KINDS = 17
 } muon_kernel_kind;
 
 int muon_profile_begin(void);

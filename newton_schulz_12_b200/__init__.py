@@ -17,7 +17,10 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import MUON_BF16, MUON_CAUTIOUS_WD, MUON_FP32, MuonError, check, ptr_array, shape_array
+from ._lib import (MUON_BF16, MUON_CAUTIOUS_WD, MUON_FP16, MUON_FP32, MuonError, check, ptr_array,
+                   shape_array)
+from .layers import (MxMatrix, muon_layer_norm, muon_layer_norm_backward, muon_mx_dequantize,
+                     muon_mx_product, muon_mx_quantize)
 
 __all__ = [
     "NS_COEFFS", "MuonError", "MuonStepPlan", "MuonNsPlan", "muon_ns_orthogonalize",
@@ -27,6 +30,8 @@ __all__ = [
     "muon_bx_apply_bf16", "muon_get_status",
     "muon_last_error", "muon_release", "muon_workspace_bytes", "muon_set_wait_timeout_ms", "muon_set_fault_injection",
     "muon_profile_begin", "muon_profile_end", "muon_version", "MUON_BF16", "MUON_FP32",
+    "MUON_FP16", "MxMatrix", "muon_layer_norm", "muon_layer_norm_backward", "muon_mx_quantize",
+    "muon_mx_dequantize", "muon_mx_product",
 ]
 
 #: Default quintic coefficients (a, b, c) of X <- aX + (bA + cA^2)X.

@@ -18,6 +18,7 @@ LIB_PATH = os.environ.get("MUON_B200_LIB") or os.path.join(
 
 MUON_BF16 = 0
 MUON_FP32 = 1
+MUON_FP16 = 2
 MUON_CAUTIOUS_WD = 1
 
 STATUS_NAMES = {
@@ -35,6 +36,7 @@ _PP = ctypes.POINTER(ctypes.c_void_p)
 _I = ctypes.c_int
 _F = ctypes.c_float
 _I64P = ctypes.POINTER(ctypes.c_int64)
+_L = ctypes.c_longlong
 
 #: name -> (restype, argtypes); every entry point of include/muon.h.
 SIGNATURES = {
@@ -50,6 +52,12 @@ SIGNATURES = {
     "muon_poly_bf16": (_I, [_I, _I, _P, _P, _F, _F, _P]),
     "muon_bx_bf16": (_I, [_I, _I, _I, _P, _P, _P, _P, _F, _P]),
     "muon_bx_apply_bf16": (_I, [_I, _I, _I, _I, _P, _I, _P, _P, _PP, _I, _F, _F, _F, _I, _P]),
+    "muon_layer_norm": (_I, [_L, _L, _P, _L, _I, _P, _P, _I, _F, _P, _L, _P, _P, _P]),
+    "muon_layer_norm_backward": (_I, [_L, _L, _P, _L, _P, _L, _I, _P, _I, _P, _P, _P, _L, _P, _P, _P, _L, _P]),
+    "muon_layer_norm_scratch_bytes": (_I, [_L, _L, ctypes.POINTER(ctypes.c_longlong)]),
+    "muon_mx_quantize": (_I, [_I, _PP, _I64P, _I64P, _I, _PP, _PP, _PP, _PP, _P]),
+    "muon_mx_dequantize": (_I, [_I, _PP, _PP, _I64P, _PP, _I, _P]),
+    "muon_mx_product": (_I, [_L, _L, _L, _P, _P, _P, _P, _P, _L, _I, _P]),
     "muon_get_status": (_I, [_P]),
     "muon_last_error": (ctypes.c_char_p, []),
     "muon_release": (_I, []),
@@ -63,7 +71,7 @@ SIGNATURES = {
 
 #: muon_kernel_kind names, in enum order.
 KERNEL_KINDS = ["flat", "cast", "gram", "poly", "bx", "out", "simt", "sums", "prep", "scale", "bx_apply",
-                "norm"]
+                "norm", "layer_norm", "layer_norm_grad", "mx_quantize", "mx_dequantize", "mx_product"]
 
 _lock = threading.Lock()
 _lib = None

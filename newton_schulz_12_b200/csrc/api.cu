@@ -13,6 +13,7 @@
 // for most of the speedup" (five Newton-Schulz steps, nearest semi-orthogonal
 // matrix).
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -79,6 +80,7 @@ std::map<std::pair<int, uintptr_t>, Workspace> g_ws;
 std::map<int, DevInfo> g_dev;
 unsigned long long g_timeout_ns = 2000000000ull;
 int g_inject = 0;
+std::atomic<bool> g_captured_launches{false};  // a captured launch without a status word of its stream
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -1270,6 +1272,95 @@ std::vector<float> constant_schedule(float a, float b, float c, int steps) {
 
 }  // namespace
 
+// What the other C-ABI file takes from this one.
+namespace muon {
+namespace host {
+
+int set_error(int code, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  t_err = buf;
+  return code;
+}
+
+void clear_error() { t_err.clear(); }
+
+int device_sms(int* sms) {
+  DevInfo dev;
+  MUON_TRY(device_info(&dev));
+  *sms = dev.sms;
+  return MUON_OK;
+}
+
+// A stream under capture that has no status word yet gets none (allocating
+// one would end the capture): null, and the kernel takes its own.
+int workspace_status(cudaStream_t s, int** status) {
+  int dev = 0;
+  CUDA_TRY(cudaGetDevice(&dev));
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    auto it = g_ws.find({dev, reinterpret_cast<uintptr_t>(s)});
+    if (it != g_ws.end() && it->second.status) {
+      *status = it->second.status;
+      return MUON_OK;
+    }
+  }
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &capture) != cudaSuccess) {
+    cudaGetLastError();  // the legacy stream while another one captures
+    capture = cudaStreamCaptureStatusActive;
+  }
+  if (capture != cudaStreamCaptureStatusNone) {
+    g_captured_launches = true;
+    *status = nullptr;
+    return MUON_OK;
+  }
+  Workspace* ws = nullptr;
+  MUON_TRY(get_workspace(s, 0, &ws));
+  *status = ws->status;
+  return MUON_OK;
+}
+
+unsigned long long wait_timeout_ns() { return g_timeout_ns; }
+
+int encode_bytes_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint64_t stride,
+                    uint32_t box_inner, uint32_t box_rows) {
+  MUON_TRY(get_encoder());
+  cuuint64_t dims[2] = {inner, rows};
+  cuuint64_t strides[1] = {stride};
+  cuuint32_t box[2] = {box_inner, box_rows};
+  cuuint32_t es[2] = {1, 1};
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return set_err(MUON_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for %llu bytes x %llu rows, box %ux%u",
+                   static_cast<int>(r), (unsigned long long)inner, (unsigned long long)rows, box_inner, box_rows);
+  return MUON_OK;
+}
+
+Timed::Timed(int kind, cudaStream_t s) : kind_(kind), s_(s), a_(nullptr) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (!g_prof_on) return;
+  a_ = take_event();
+  if (a_) cudaEventRecord(a_, s_);
+}
+
+Timed::~Timed() {
+  if (!a_) return;
+  std::lock_guard<std::mutex> lk(g_mu);
+  cudaEvent_t b = take_event();
+  if (!b) return;
+  cudaEventRecord(b, s_);
+  g_prof.push_back({kind_, a_, b});
+}
+
+}  // namespace host
+}  // namespace muon
+
 extern "C" {
 
 int muon_ns_orthogonalize(int batch, int m, int n, void* const* X_ptrs, float a, float b, float c,
@@ -1569,6 +1660,12 @@ int muon_get_status(void* stream) {
   CUDA_TRY(cudaStreamSynchronize(s));
   int dev = 0;
   CUDA_TRY(cudaGetDevice(&dev));
+  if (g_captured_launches) {
+    int captured = 0;
+    CUDA_TRY(mx::take_captured_status(&captured));
+    if (captured != 0)
+      return set_err(captured, "device status %d (a bounded device-side wait ran out in a captured launch)", captured);
+  }
   int* st = nullptr;
   {
     std::lock_guard<std::mutex> lk(g_mu);

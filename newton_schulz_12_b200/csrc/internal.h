@@ -341,4 +341,141 @@ cudaError_t launch_norm_factors(const NormFacParams& p, cudaStream_t s);
 
 }  // namespace ew
 
+// ------------------------------------------------------------------ layer norm
+// Types are muon_dtype values (0 bf16, 1 fp32, 2 fp16) here and below.
+namespace ln {
+
+struct FwdParams {
+  long long rows;
+  int cols;
+  const void* x;
+  long long ldx;
+  const void* weight;  // or null: 1
+  const void* bias;    // or null: 0
+  float eps;
+  void* y;
+  long long ldy;
+  float* mean;
+  float* rstd;
+};
+
+struct BwdParams {
+  long long rows;
+  int cols;
+  const void* dy;
+  long long lddy;
+  const void* x;
+  long long ldx;
+  const void* weight;  // or null: 1
+  const float* mean;
+  const float* rstd;
+  void* dx;
+  long long lddx;
+  void* dweight;       // or null: not wanted
+  void* dbias;         // or null: not wanted
+  float* partials;     // parts x 2 x cols: partial sums of dy xhat, then of dy
+  int parts;
+};
+
+// Partial sums that a backward pass of this size writes (0 for no rows).
+int partial_count(long long rows, int cols, int sms);
+cudaError_t launch_forward(const FwdParams& p, int dtype, int param_dtype, int sms, cudaStream_t s);
+cudaError_t launch_backward(const BwdParams& p, int dtype, int param_dtype, int sms, cudaStream_t s);
+
+}  // namespace ln
+
+// ------------------------------------------- 4-bit microscaled (MX) matrices
+// E2M1 values in blocks of 32 along a row, one power-of-two scale byte a block.
+// data: rows of 16 * ceil(cols / 32) bytes.  scales: tiles of 128 rows x 4
+// blocks, 512 bytes each, [row tile][block tile][row % 32][row % 128 / 32][block % 4],
+// the order in which the tensor cores take them.
+namespace mx {
+
+constexpr int kMaxMats = 64;  // matrices per launch
+constexpr int kTile = 128;    // rows and columns of a quantise tile
+
+__host__ __device__ inline long long data_stride(long long cols) { return (cols + 31) / 32 * 16; }
+
+struct QuantMat {
+  const void* x;
+  long long ldx;
+  int rows, cols;
+  int tiles_c;      // 128-wide tiles along the columns
+  int tile_begin;
+  void* row_data;   // blocks along the rows, or null
+  void* row_scales;
+  void* col_data;   // blocks along the columns (the transpose's rows), or null
+  void* col_scales;
+};
+
+struct QuantParams {
+  QuantMat mat[kMaxMats];
+  int nmat, ntiles;
+};
+
+struct DequantMat {
+  const void* data;
+  const void* scales;
+  void* y;
+  int rows, cols;
+  int tiles_c;
+  int tile_begin;
+};
+
+struct DequantParams {
+  DequantMat mat[kMaxMats];
+  int nmat, ntiles;
+};
+
+cudaError_t launch_quantize(const QuantParams& p, int dtype, int sms, cudaStream_t s);
+cudaError_t launch_dequantize(const DequantParams& p, int dtype, int sms, cudaStream_t s);
+
+// C = A B^T, A m x k and B n x k in 4 bits.
+struct ProductParams {
+  CUtensorMap a, b;      // data, bytes, 128-byte swizzle
+  const void* a_scales;
+  const void* b_scales;
+  void* out;
+  long long ldo;
+  int m, n, k;
+  int transposed;        // 1: a, m are the caller's B and n: out[col * ldo + row]
+  int* status;
+  unsigned long long timeout_ns;
+};
+
+// Rows of the tile that the b map's box has to cover for an m x n product.
+int product_tile_n(int m, int n);
+cudaError_t launch_product(const ProductParams& p, int dtype, int sms, cudaStream_t s);
+// Reads and clears the current device's status word of captured launches.
+cudaError_t take_captured_status(int* value);
+
+}  // namespace mx
+
+// ------------------------------------------------ shared by the C-ABI files
+namespace host {
+
+int set_error(int code, const char* fmt, ...);
+void clear_error();
+int device_sms(int* sms);                       // checks the device, too
+int workspace_status(cudaStream_t s, int** status);  // device status word of (current device, stream)
+unsigned long long wait_timeout_ns();
+int encode_bytes_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint64_t stride,
+                    uint32_t box_inner, uint32_t box_rows);
+
+// Brackets one launch with events while kernel timing is on.
+class Timed {
+ public:
+  Timed(int kind, cudaStream_t s);
+  ~Timed();
+  Timed(const Timed&) = delete;
+  Timed& operator=(const Timed&) = delete;
+
+ private:
+  int kind_;
+  cudaStream_t s_;
+  cudaEvent_t a_;
+};
+
+}  // namespace host
+
 }  // namespace muon

@@ -1,0 +1,375 @@
+// C = A B^T of two 4-bit microscaled matrices on the tensor cores
+// (tcgen05.mma kind::mxf4, one scale byte for every 32 values along k).
+//
+// A CTA holds a 128 x BN tile of C in tensor memory.  Warp 0 copies the
+// operands' data (128-byte swizzled boxes of 128 bytes = 256 values along k)
+// and their scales (512-byte tiles of 128 rows x 4 blocks, already in the
+// order that tcgen05.cp wants) into a ring; one thread of warp 1 copies each
+// stage's scales on to tensor memory and issues the products; four warps
+// convert and store the finished tile while the next one is computed in the
+// second accumulator.
+#include "common.cuh"
+#include "internal.h"
+
+#include <cuda_fp16.h>
+
+namespace muon {
+namespace mx {
+
+namespace {
+
+constexpr int BM = 128;
+constexpr int kStageK = 256;           // values of k a stage: 128 bytes of data a row
+constexpr int kThreads = 192;          // copier, issuer, four epilogue warps
+constexpr int kScaleTile = 512;        // bytes: 128 rows x 4 blocks
+
+// Where a wait that runs out in a captured launch is recorded when the stream
+// had no status word at capture (see workspace_status).
+__device__ int g_captured_status;
+
+template <int BN>
+struct Cfg {
+  static constexpr int kScaleTilesB = (BN + 127) / 128;
+  static constexpr uint32_t kABytes = BM * 128;
+  static constexpr uint32_t kBBytes = BN * 128;
+  static constexpr uint32_t kScaleA = 2 * kScaleTile;  // two tiles along k
+  static constexpr uint32_t kScaleB = 2 * kScaleTile * kScaleTilesB;
+  static constexpr uint32_t kStageBytes = kABytes + kBBytes + kScaleA + kScaleB;
+  static constexpr int kStages = 5;
+  static constexpr uint32_t kStageRow = 64 * 4 + 16;  // staging row: 64 values, padded against bank conflicts
+  static constexpr uint32_t kStagingWarp = 32 * kStageRow;
+  // full, empty per stage; tfull, tempty x 2; scale slots x 2; drain
+  static constexpr int kBars = 2 * kStages + 7;
+  static constexpr size_t kSmem = 1024 + kStages * kStageBytes + 4 * kStagingWarp + kBars * 8 + 16;
+  // tensor memory columns: two accumulators, then two slots of a stage's scales
+  static constexpr uint32_t kScaleCol = 2 * BN;
+  static constexpr uint32_t kColsA = 2 * 4, kColsB = 2 * 4 * kScaleTilesB;  // 4 columns a tile
+  static constexpr uint32_t kSlotCols = kColsA + kColsB;
+  static_assert(kScaleCol + 2 * kSlotCols <= 512, "tensor memory");
+  static_assert(kSmem <= 232448, "shared memory");
+  static_assert(kStageBytes % 1024 == 0, "swizzled boxes start on 1 KiB");
+};
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* map, uint32_t bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+      : "memory");
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+// One tile of scales (32 rows of 16 bytes) to four columns of tensor memory,
+// the same in each quarter of the lanes: row 32 j + i of the operand is byte
+// group j of lane i.
+__device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint32_t saddr) {
+  uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(128u >> 4) << 32;  // 8-row groups of 16-byte rows; no swizzle
+  d |= 1ull << 46;
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+
+// Instruction descriptor of kind::mxf4: E2M1 operands, power-of-two scales,
+// fp32 sums, M x N; `id` is the first of the two scale bytes in a column's four.
+__host__ __device__ constexpr uint32_t idesc_mxf4(int m, int n, int id) {
+  return (static_cast<uint32_t>(id) << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (1u << 23) | (static_cast<uint32_t>(m >> 7) << 27) | (static_cast<uint32_t>(id) << 29);
+}
+
+__device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+      : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ T rounded(float v);
+template <>
+__device__ __forceinline__ float rounded<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ bf16 rounded<bf16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half rounded<__half>(float v) { return __float2half_rn(v); }
+
+template <int BN, typename T, bool TRANS>
+__global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ ProductParams p) {
+  using C = Cfg<BN>;
+  constexpr int S = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* staging = smem + S * C::kStageBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + 4 * C::kStagingWarp);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::kBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t bar0 = smem_u32(bars), smem0 = smem_u32(smem);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (S + s); };
+  auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * S + a); };
+  auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * S + 2 + a); };
+  auto slot_bar = [&](int a) { return bar0 + 8u * (2 * S + 4 + a); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * S + 6);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), 4);
+      mbar_init(slot_bar(a), 1);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_holder), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+
+  WaitCtl ctl;
+  ctl.abort_flag = abort_flag;
+  ctl.status = p.status ? p.status : &g_captured_status;
+  ctl.timeout_ns = p.timeout_ns;
+  ctl.where = 0;
+  ctl.peer_abort = 0;
+  const unsigned long long drain_ns = p.timeout_ns < 50000000ull ? p.timeout_ns : 50000000ull;
+
+  const int tiles_m = (p.m + BM - 1) / BM, tiles_n = (p.n + BN - 1) / BN;
+  const int tiles = tiles_m * tiles_n;
+  const int kiters = (p.k + kStageK - 1) / kStageK;
+  const int ktiles = (p.k + 127) / 128;        // scale tiles along k
+  const int rows_b = (p.n + 127) / 128;        // scale tiles along B's rows
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, parity = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        const int tm = t % tiles_m, tn = t / tiles_m;
+        const int first_b = tn * BN / 128;
+        const int nb = min(C::kScaleTilesB, rows_b - first_b);
+        for (int it = 0; it < kiters; ++it) {
+          if (!mbar_wait(empty_bar(stage), phase ^ 1u, ctl)) {
+            ok = false;
+            break;
+          }
+          const int kt = min(2, ktiles - 2 * it);  // scale tiles of this stage along k
+          const uint32_t sbytes = static_cast<uint32_t>(kt) * kScaleTile;
+          mbar_arrive_expect_tx(full_bar(stage), C::kABytes + C::kBBytes + sbytes * (1 + nb));
+          issued |= 1u << stage;
+          parity = (parity & ~(1u << stage)) | (phase << stage);
+          const uint32_t a = smem0 + stage * C::kStageBytes, b = a + C::kABytes, sa = b + C::kBBytes, sb = sa + C::kScaleA;
+          tma_load_2d(a, &p.a, full_bar(stage), it * 128, tm * BM);
+          tma_load_2d(b, &p.b, full_bar(stage), it * 128, tn * BN);
+          bulk_load(sa, static_cast<const uint8_t*>(p.a_scales) + (static_cast<long long>(tm) * ktiles + 2 * it) * kScaleTile,
+                    sbytes, full_bar(stage));
+          for (int j = 0; j < nb; ++j)
+            bulk_load(sb + j * 2 * kScaleTile,
+                      static_cast<const uint8_t*>(p.b_scales) + (static_cast<long long>(first_b + j) * ktiles + 2 * it) * kScaleTile,
+                      sbytes, full_bar(stage));
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok)
+        for (int s = 0; s < S; ++s)
+          if (issued & (1u << s)) mbar_wait_drain(full_bar(s), (parity >> s) & 1u, drain_ns);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int stage = 0, acc = 0, slot = 0;
+      uint32_t phase = 0, acc_phase = 0, slot_phase = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        if (!mbar_wait(tempty_bar(acc), acc_phase ^ 1u, ctl)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + static_cast<uint32_t>(acc * BN);
+        const uint32_t group = static_cast<uint32_t>((t / tiles_m) * BN % 128) / 32;  // first 32 rows of B in its scale tile
+        for (int it = 0; it < kiters; ++it) {
+          // the slot's scales were last read by the products of two stages ago
+          if (!mbar_wait(full_bar(stage), phase, ctl) || !mbar_wait(slot_bar(slot), slot_phase ^ 1u, ctl)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = smem0 + stage * C::kStageBytes, b = a + C::kABytes, sa = b + C::kBBytes, sb = sa + C::kScaleA;
+          const uint32_t ta = tmem + C::kScaleCol + static_cast<uint32_t>(slot) * C::kSlotCols, tb = ta + C::kColsA;
+          const int steps = min(4, (p.k - it * kStageK + 63) / 64);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (2 * h >= steps) break;
+            scales_to_tmem(ta + 4 * h, sa + h * kScaleTile);
+#pragma unroll
+            for (int j = 0; j < C::kScaleTilesB; ++j)
+              scales_to_tmem(tb + (h * C::kScaleTilesB + j) * 4, sb + (2 * j + h) * kScaleTile);
+          }
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            if (kk >= steps) break;
+            const uint32_t h = kk >> 1;
+            mma_mxf4(d, sdesc_sw128(a + kk * 32, 16, 1024), sdesc_sw128(b + kk * 32, 16, 1024),
+                     idesc_mxf4(BM, BN, 2 * (kk & 1)), ta + 4 * h, tb + h * C::kScaleTilesB * 4 + group,
+                     (it | kk) != 0 ? 1u : 0u);
+          }
+          tc_commit(empty_bar(stage));
+          tc_commit(slot_bar(slot));
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          if (++slot == 2) {
+            slot = 0;
+            slot_phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        tc_commit(tfull_bar(acc));
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+      tc_commit(drain_bar);
+      mbar_wait_drain(drain_bar, 0, drain_ns > 1000000ull ? drain_ns : 1000000ull);
+    }
+    __syncwarp();
+  } else {
+    const int quarter = warp & 3;
+    uint8_t* stg = staging + quarter * C::kStagingWarp;
+    T* out = static_cast<T*>(p.out);
+    constexpr int kVec = 16 / sizeof(T);
+    const bool vec = (reinterpret_cast<uintptr_t>(out) % 16 == 0) && (p.ldo % kVec == 0);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+      const int tm = t % tiles_m, tn = t / tiles_m;
+      const bool ok = mbar_wait(tfull_bar(acc), acc_phase, ctl);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      tc_fence_after();
+      const long long row0 = static_cast<long long>(tm) * BM + quarter * 32;
+      constexpr int CW = BN < 64 ? BN : 64;
+      for (int c0 = 0; c0 < BN; c0 += CW) {
+        const long long col0 = static_cast<long long>(tn) * BN + c0;
+#pragma unroll
+        for (int h = 0; h < CW / 32; ++h) {
+          uint32_t r[32];
+          tmem_ld_32x32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * BN + c0 + 32 * h), r);
+          tmem_ld_wait();
+          if (TRANS) {
+            if (row0 + lane < p.m)
+              for (int j = 0; j < 32; ++j)
+                if (col0 + 32 * h + j < p.n) out[(col0 + 32 * h + j) * p.ldo + row0 + lane] = rounded<T>(__uint_as_float(r[j]));
+          } else {
+            T* mine = reinterpret_cast<T*>(stg + lane * C::kStageRow) + 32 * h;
+#pragma unroll
+            for (int j = 0; j < 32; j += kVec) {
+              T v[kVec];
+#pragma unroll
+              for (int q = 0; q < kVec; ++q) v[q] = rounded<T>(__uint_as_float(r[j + q]));
+              *reinterpret_cast<uint4*>(mine + j) = *reinterpret_cast<const uint4*>(v);
+            }
+          }
+        }
+        if (!TRANS) {
+          __syncwarp();
+          if (vec && col0 + CW <= p.n) {
+            constexpr int per_row = CW / kVec;
+            for (int e = lane; e < 32 * per_row; e += 32) {
+              const int r = e / per_row, u = e % per_row;
+              if (row0 + r < p.m)
+                *reinterpret_cast<uint4*>(out + (row0 + r) * p.ldo + col0 + u * kVec) =
+                    *reinterpret_cast<const uint4*>(stg + r * C::kStageRow + u * 16);
+            }
+          } else {
+            for (int e = lane; e < 32 * CW; e += 32) {
+              const int r = e / CW, c = e % CW;
+              if (row0 + r < p.m && col0 + c < p.n)
+                out[(row0 + r) * p.ldo + col0 + c] = reinterpret_cast<const T*>(stg + r * C::kStageRow)[c];
+            }
+          }
+          __syncwarp();
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tempty_bar(acc));
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int BN, typename T, bool TRANS>
+cudaError_t launch_one(const ProductParams& p, int sms, cudaStream_t s) {
+  static thread_local int configured_device = -1;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (configured_device != dev) {
+    cudaError_t e = cudaFuncSetAttribute(product_kernel<BN, T, TRANS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(Cfg<BN>::kSmem));
+    if (e != cudaSuccess) return e;
+    configured_device = dev;
+  }
+  const long long tiles = static_cast<long long>((p.m + BM - 1) / BM) * ((p.n + BN - 1) / BN);
+  product_kernel<BN, T, TRANS><<<static_cast<int>(tiles < sms ? tiles : sms), kThreads, Cfg<BN>::kSmem, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_typed(const ProductParams& p, int sms, cudaStream_t s) {
+  switch (product_tile_n(p.m, p.n)) {
+    case 32: return p.transposed ? launch_one<32, T, true>(p, sms, s) : launch_one<32, T, false>(p, sms, s);
+    case 64: return p.transposed ? launch_one<64, T, true>(p, sms, s) : launch_one<64, T, false>(p, sms, s);
+    default: return launch_one<128, T, false>(p, sms, s);
+  }
+}
+
+}  // namespace
+
+// m is the larger side where the smaller one has at most 64 rows.
+int product_tile_n(int m, int n) {
+  (void)m;
+  return n <= 32 ? 32 : n <= 64 ? 64 : 128;
+}
+
+cudaError_t launch_product(const ProductParams& p, int dtype, int sms, cudaStream_t s) {
+  return dtype == 1 ? launch_typed<float>(p, sms, s) : dtype == 0 ? launch_typed<bf16>(p, sms, s) : launch_typed<__half>(p, sms, s);
+}
+
+cudaError_t take_captured_status(int* value) {
+  cudaError_t e = cudaMemcpyFromSymbol(value, g_captured_status, sizeof(int));
+  if (e != cudaSuccess || *value == 0) return e;
+  const int zero = 0;
+  return cudaMemcpyToSymbol(g_captured_status, &zero, sizeof(int));
+}
+
+}  // namespace mx
+}  // namespace muon
