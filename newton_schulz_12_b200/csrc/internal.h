@@ -374,10 +374,10 @@ struct BwdParams {
   void* dweight;       // or null: not wanted
   void* dbias;         // or null: not wanted
   float* partials;     // parts x 2 x cols: partial sums of dy xhat, then of dy
-  int parts;
+  int parts;           // partial_count, or 0: neither sum is wanted
 };
 
-// Partial sums that a backward pass of this size writes (0 for no rows).
+// Partial sums that a backward pass of this size writes at most (0 for no rows).
 int partial_count(long long rows, int cols, int sms);
 cudaError_t launch_forward(const FwdParams& p, int dtype, int param_dtype, int sms, cudaStream_t s);
 cudaError_t launch_backward(const BwdParams& p, int dtype, int param_dtype, int sms, cudaStream_t s);

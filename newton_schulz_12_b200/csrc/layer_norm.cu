@@ -177,16 +177,31 @@ __global__ void __launch_bounds__(1024) finish_kernel(const BwdParams p) {
 }
 
 // ---------------------------------------------------------------------------
-// Rows held in registers.  A row is the work of `tpr` threads (8, 16 or whole
-// warps) with E = VEC * NV values each, a block has `groups` such groups and
-// walks over the rows, with the next row's loads issued before this one is
-// worked on.  VEC values are one 16-byte access where rows, parameters and
-// results are aligned for it, else VEC = 1.  What bounds it beside the bytes is
-// the issue of instructions: a row's sums cost the same for 8 values a thread
-// as for 32, so a row takes as few warps as hold it.
+// Rows held on chip.  A row is the work of `tpr` threads (8, 16 or whole warps)
+// with E = VEC * NV values each; a block has `groups` such groups and walks over
+// the rows, two values an instruction (f32x2).
+//
+// RING: every thread copies its own values of the next rows into its own places
+// of a ring in shared memory (cp.async: a thread waits for nobody else) and
+// works on a row from registers.  Else a row is loaded straight into registers:
+// for launches of few rows, which the ring's set-up costs more than it gives
+// (1 x 768 bf16: 2.4 us against 4.7), and for 16-bit rows that start on no 16
+// bytes, whose values would each take a 4-byte copy (16381 x 1021 bf16: 28.9 us
+// against 42.3).
+//
+// What bounds it: bytes in flight first (about 40 KB an SM cover the latency),
+// then the issue of instructions.  A row's sums cost the same for 8 values a
+// thread as for 32, so a row takes as few warps as hold it.  The parameters are
+// laid out in shared memory once, in the order in which threads read them: read
+// from L1 as fp32, 32 bytes a lane, they kept it at 80 % of its throughput.
+//
+// VEC values are one 16-byte access where rows and results are aligned for it,
+// else VEC = 1.
 // ---------------------------------------------------------------------------
 constexpr int kFwdE = 32, kFwdThreads = 512;  // values a thread, threads a block: at most
-constexpr int kBwdE = 24, kBwdThreads = 384;  // with the column sums: 168 registers a thread
+constexpr int kBwdE = 24, kBwdThreads = 384;  // with the column sums
+constexpr int kMaxDepth = 4;                  // ring slots
+constexpr int kSmemBudget = 212 * 1024;       // of an SM, for its blocks' rings and parameters
 
 template <typename T, int VEC>
 struct Pack;  // VEC values of one access
@@ -199,11 +214,101 @@ struct __align__(16) Pack {
   T v[VEC];
 };
 
-// A streamed access, zeros where `ok` is false; it bypasses L1, which keeps the
-// parameters.  Predicated within one statement: with a branch around the load
-// the zeros would meet it in a register move that waits for it, so that a
-// row's loads came one after the other (229 us instead of 96 for the gradient
-// of 8192 x 8192 bf16).
+// Two fp32 values in one register pair: the packed operations of common.cuh
+// work on both at once, each rounded as alone.
+typedef unsigned long long f32x2;
+
+template <typename T>
+__device__ __forceinline__ f32x2 widen(T lo, T hi) { return f2(to_f(lo), to_f(hi)); }
+
+template <typename T>
+__device__ __forceinline__ void narrow(f32x2 v, T* out);
+template <>
+__device__ __forceinline__ void narrow<float>(f32x2 v, float* out) { f2_split(v, out[0], out[1]); }
+template <>
+__device__ __forceinline__ void narrow<bf16>(f32x2 v, bf16* out) {
+  float lo, hi;
+  f2_split(v, lo, hi);
+  *reinterpret_cast<__nv_bfloat162*>(out) = __floats2bfloat162_rn(lo, hi);
+}
+template <>
+__device__ __forceinline__ void narrow<__half>(f32x2 v, __half* out) {
+  float lo, hi;
+  f2_split(v, lo, hi);
+  *reinterpret_cast<__half2*>(out) = __floats2half2_rn(lo, hi);
+}
+
+// 1 / sqrt(v): the hardware's estimate (2 fp32 units) and one Newton step, left
+// out where it would make a NaN of 0 or an infinity.
+__device__ __forceinline__ float reciprocal_root(float v) {
+  const float y = rsqrtf(v), z = y * fmaf(-0.5f * v * y, y, 1.5f);
+  return v > 0.f && y > 0.f ? z : y;
+}
+
+__device__ __forceinline__ float both(f32x2 v) {
+  float lo, hi;
+  f2_split(v, lo, hi);
+  return lo + hi;
+}
+
+// This thread's places for one row a slot: slot s, vector j.
+template <typename T, int VEC, int NV>
+struct Ring {
+  static constexpr int kPlace = VEC > 1 ? 16 : 4;
+  static constexpr int kRow = NV * kPlace;  // bytes of a row a thread
+  uint32_t base, vec;  // shared address of slot 0, vector 0; bytes from vector to vector
+  int nv;              // vectors of the thread within the row: at t, t + tpr, ...
+
+  __device__ __forceinline__ Ring(uint32_t start, int threads, int nv_)
+      : base(start + threadIdx.x * kPlace), vec(threads * kPlace), nv(nv_) {}
+
+  // Starts the copy of this thread's values of a row; `at`: its first value's
+  // address (any valid one if it has none).  Vectors beyond the row, and all of
+  // them where `in` is false, become zeros.
+  __device__ __forceinline__ void start(int slot, const T* at, int tpr, bool in) const {
+    uint32_t dst = base + static_cast<uint32_t>(slot * NV) * vec;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const bool ok = in && j < nv;
+      const T* src = at + (j < nv ? j * tpr * VEC : 0);
+      if constexpr (VEC > 1)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+      else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0) : "memory");
+      dst += vec;
+    }
+  }
+
+  // The values of a slot's row, in fp32 pairs.
+  __device__ __forceinline__ void read(int slot, f32x2 (&out)[VEC * NV / 2]) const {
+    uint32_t src = base + static_cast<uint32_t>(slot * NV) * vec;
+    if constexpr (VEC > 1) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        uint4 r;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(src));
+        const Pack<T, VEC> v = *reinterpret_cast<const Pack<T, VEC>*>(&r);
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) out[(j * VEC + i) / 2] = widen<T>(v.v[i], v.v[i + 1]);
+        src += vec;
+      }
+    } else {
+      float v[NV];
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[j]) : "r"(src));
+        src += vec;
+      }
+#pragma unroll
+      for (int j = 0; j < NV; j += 2) out[j / 2] = f2(v[j], v[j + 1]);
+    }
+  }
+};
+
+// A value's access straight into a register, zero where `ok` is false.
+// Predicated within one statement: with a branch around the load the zero would
+// meet it in a register move that waits for it, so that a row's loads came one
+// after the other (8192 x 8192 bf16, gradient: 229 us against 96).
 template <typename T, int VEC>
 __device__ __forceinline__ void load_pack(Pack<T, VEC>& out, const T* src, bool ok) {
   if constexpr (VEC > 1) {
@@ -230,47 +335,104 @@ __device__ __forceinline__ void load_pack(Pack<T, VEC>& out, const T* src, bool 
   }
 }
 
+// The thread's values of a row at `at`, in registers.
 template <typename T, int VEC, int NV>
 struct Held {
   Pack<T, VEC> raw[NV];
-  // `nv` vectors of the thread lie in the row: at t, t + tpr, ...
-  __device__ __forceinline__ void load(const T* row, int t, int tpr, int nv) {
-    const T* at = row + t * VEC;
+  __device__ __forceinline__ void load(const T* at, int tpr, int nv) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       load_pack(raw[j], at, j < nv);
       at += tpr * VEC;
     }
   }
-  __device__ __forceinline__ float get(int k) const { return to_f(raw[k / VEC].v[k % VEC]); }
+  __device__ __forceinline__ void read(f32x2 (&out)[VEC * NV / 2]) const {
+#pragma unroll
+    for (int k = 0; k < VEC * NV / 2; ++k)
+      out[k] = widen<T>(raw[2 * k / VEC].v[2 * k % VEC], raw[(2 * k + 1) / VEC].v[(2 * k + 1) % VEC]);
+  }
 };
 
-// A parameter vector's values of this thread's columns, `fill` where there is none.
+__device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the newest `n` rows of this thread have landed.
+__device__ __forceinline__ void ring_wait(int n) {
+  switch (n) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+  }
+}
+
+// A parameter vector in shared memory, in fp32: values 4 q .. 4 q + 3 of thread
+// t of a row at float4 q * tpr + t, `fill` where there is none or beyond the
+// row.  Eight float4 a thread are read before the first is written: one at a
+// time, a launch of few rows waited for them about 9 us.
 template <typename P, int VEC, int NV>
-__device__ __forceinline__ void load_params(float* out, const void* src, float fill, int t, int tpr, int nv) {
+__device__ __forceinline__ void stage_params(float* dst, const void* src, float fill, int tpr, int cols) {
+  constexpr int kBatch = 8;
+  const P* __restrict__ par = static_cast<const P*>(src);
+  const int total = VEC * NV / 4 * tpr;
+  for (int e0 = threadIdx.x; e0 < total; e0 += kBatch * blockDim.x) {
+    float v[kBatch][4];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = (t + j * tpr) * VEC;
+    for (int i = 0; i < kBatch; ++i) {
+      const int e = e0 + i * blockDim.x, q = e / tpr, t = e - q * tpr;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) out[j * VEC + i] = fill;
-    if (src && j < nv) {
-      constexpr int W = VEC == 1 ? 1 : 16 / static_cast<int>(sizeof(P));  // values an access of P
-#pragma unroll
-      for (int i = 0; i < VEC; i += W) {
-        const Pack<P, W> w = *reinterpret_cast<const Pack<P, W>*>(static_cast<const P*>(src) + c + i);
-#pragma unroll
-        for (int q = 0; q < (W < VEC ? W : VEC); ++q) out[j * VEC + i + q] = to_f(w.v[q]);
+      for (int h = 0; h < 4; ++h) {
+        const int k = 4 * q + h, c = (t + (k / VEC) * tpr) * VEC + k % VEC;
+        v[i][h] = par && e < total && c < cols ? to_f(par[c]) : fill;
       }
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int e = e0 + i * blockDim.x;
+      if (e < total) reinterpret_cast<float4*>(dst)[e] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
     }
   }
 }
 
-template <typename T, int VEC>
-__device__ __forceinline__ void store(T* row, int c, const float* v) {
-  Pack<T, VEC> out;
+// Without a ring: a thread's values straight from memory (anything beyond the row).
+template <typename P, int VEC, int NV>
+__device__ __forceinline__ void load_params(f32x2* out, const void* src, float fill, int t, int tpr, int nv) {
+  const P* par = static_cast<const P*>(src);
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) out.v[i] = from_f<T>(v[i]);
-  *reinterpret_cast<Pack<T, VEC>*>(row + c) = out;
+  for (int k = 0; k < VEC * NV / 2; ++k) {
+    const int j0 = 2 * k / VEC, j1 = (2 * k + 1) / VEC;
+    const int c0 = j0 < nv ? (t + j0 * tpr) * VEC + 2 * k % VEC : 0, c1 = j1 < nv ? (t + j1 * tpr) * VEC + (2 * k + 1) % VEC : 0;
+    out[k] = par ? widen<P>(par[c0], par[c1]) : f2(fill, fill);
+  }
+}
+
+__device__ __forceinline__ void read_params(const float* src, int q, int tpr, int t, f32x2& lo, f32x2& hi) {
+  const float4 v = reinterpret_cast<const float4*>(src)[q * tpr + t];
+  lo = f2(v.x, v.y);
+  hi = f2(v.z, v.w);
+}
+
+// The thread's values to its columns of a row.
+template <typename T, int VEC, int NV>
+__device__ __forceinline__ void store_row(T* row, int t, int tpr, int nv, const f32x2* v) {
+  T* at = row + t * VEC;
+  if constexpr (VEC > 1) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      Pack<T, VEC> out;
+#pragma unroll
+      for (int i = 0; i < VEC; i += 2) narrow<T>(v[(j * VEC + i) / 2], out.v + i);
+      if (j < nv) *reinterpret_cast<Pack<T, VEC>*>(at) = out;
+      at += tpr * VEC;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; j += 2) {
+      __align__(8) T out[2];
+      narrow<T>(v[j / 2], out);
+      if (j < nv) at[0] = out[0];
+      if (j + 1 < nv) at[tpr] = out[1];
+      at += 2 * tpr;
+    }
+  }
 }
 
 // Sums over the threads of a row (the same order in every thread).  `buf` is
@@ -299,140 +461,236 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float (*buf)[32], int t
   }
 }
 
-template <typename T, typename P, int VEC, int NV>
-__global__ void __launch_bounds__(kFwdThreads) forward_kernel(const FwdParams p, int tpr, int groups) {
+// R rows of a group at a time: their sums overlap, and they share the reads of
+// the parameters.
+template <typename T, typename P, int VEC, int NV, int R, bool RING>
+__global__ void __launch_bounds__(kFwdThreads) forward_kernel(const FwdParams p, int tpr, int groups, int depth) {
   constexpr int E = VEC * NV;
-  constexpr bool kKeep = E <= 8;     // parameters stay in registers
-  constexpr bool kAhead = VEC > 1;   // one-value accesses have enough in flight, and no registers to spare
-  __shared__ float buf[2][1][32];
+  __shared__ float buf[2][R][32];
+  extern __shared__ __align__(16) uint8_t smem[];
   const int g = threadIdx.x / tpr, t = threadIdx.x - g * tpr;
-  const long long step = static_cast<long long>(gridDim.x) * groups;
+  const long long step = static_cast<long long>(gridDim.x) * groups * R;
   const int nv = max(0, (p.cols - t * VEC + tpr * VEC - 1) / (tpr * VEC));
-  float w[E], b[E];
-  if (kKeep) {
-    load_params<P, VEC, NV>(w, p.weight, 1.f, t, tpr, nv);
-    load_params<P, VEC, NV>(b, p.bias, 0.f, t, tpr, nv);
-  }
   const float inv = 1.0f / p.cols;
-  Held<T, VEC, NV> next;
-  long long r = static_cast<long long>(blockIdx.x) * groups + g;
-  if (kAhead) next.load(static_cast<const T*>(p.x) + r * p.ldx, t, tpr, r < p.rows ? nv : 0);
-  for (long long base = static_cast<long long>(blockIdx.x) * groups; base < p.rows; base += step) {
-    r = base + g;
-    const bool ok = r < p.rows;
-    if (!kAhead) next.load(static_cast<const T*>(p.x) + r * p.ldx, t, tpr, ok ? nv : 0);
-    float x[E];
-    float s[1] = {0.f};
+  const T* x0 = static_cast<const T*>(p.x) + (nv ? t * VEC : 0);
+  const Ring<T, VEC, NV> ring(smem_u32(smem), blockDim.x, nv);
+  float* wsm = reinterpret_cast<float*>(smem + static_cast<size_t>(depth) * R * blockDim.x * ring.kRow);
+  float* bsm = wsm + E * tpr;
+  const long long first = static_cast<long long>(blockIdx.x) * groups * R;
+  long long ahead = first + g * R;  // the next rows to start, and their slot
+  int head = 0;
+  auto start = [&] {
 #pragma unroll
-    for (int k = 0; k < E; ++k) {
-      x[k] = next.get(k);
-      s[0] += x[k];
+    for (int i = 0; i < R; ++i) {
+      const bool in = ahead + i < p.rows;
+      ring.start(head * R + i, in ? x0 + (ahead + i) * p.ldx : x0, tpr, in);
     }
-    if (kAhead) next.load(static_cast<const T*>(p.x) + (r + step) * p.ldx, t, tpr, r + step < p.rows ? nv : 0);
-    group_sum(s, buf[0], tpr, g, t);
-    const float mean = s[0] * inv;
-    float q[1] = {0.f};
+    ring_commit();
+    ahead += step;
+    if (++head == depth) head = 0;
+  };
+  if constexpr (RING) {
+    for (int i = 1; i < depth; ++i) start();
+    stage_params<P, VEC, NV>(wsm, p.weight, 1.f, tpr, p.cols);
+    stage_params<P, VEC, NV>(bsm, p.bias, 0.f, tpr, p.cols);
+    __syncthreads();
+  }
+  int slot = 0;
+  for (long long base = first; base < p.rows; base += step) {
+    const long long r = base + g * R;
+    f32x2 x[R][E / 2], wreg[RING ? 1 : E / 2], breg[RING ? 1 : E / 2];
+    Held<T, VEC, NV> held[RING ? 1 : R];
+    if constexpr (RING) {
+      start();
+      ring_wait(depth - 1);
+    } else {
 #pragma unroll
-    for (int k = 0; k < E; ++k) {
-      x[k] = k / VEC < nv ? x[k] - mean : 0.f;
-      q[0] = fmaf(x[k], x[k], q[0]);
+      for (int i = 0; i < R; ++i) held[i].load(x0 + (r + i < p.rows ? (r + i) * p.ldx : 0), tpr, r + i < p.rows ? nv : 0);
+      load_params<P, VEC, NV>(wreg, p.weight, 1.f, t, tpr, nv);
+      load_params<P, VEC, NV>(breg, p.bias, 0.f, t, tpr, nv);
+    }
+    float s[R], q[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if constexpr (RING)
+        ring.read(slot * R + i, x[i]);
+      else
+        held[i].read(x[i]);
+      f32x2 a = x[i][0];
+#pragma unroll
+      for (int k = 1; k < E / 2; ++k) a = f2_add(a, x[i][k]);
+      s[i] = both(a);
+    }
+    if (RING && ++slot == depth) slot = 0;
+    group_sum(s, buf[0], tpr, g, t);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      s[i] *= inv;
+      const f32x2 m = f2(s[i], s[i]);
+      f32x2 a = f2(0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < E / 2; ++k) {
+        if (VEC > 1) {
+          if (2 * k / VEC < nv) {
+            x[i][k] = f2_sub(x[i][k], m);
+            a = f2_fma(x[i][k], x[i][k], a);
+          }
+        } else {
+          float lo, hi;
+          f2_split(f2_sub(x[i][k], m), lo, hi);
+          x[i][k] = f2(2 * k < nv ? lo : 0.f, 2 * k + 1 < nv ? hi : 0.f);
+          a = f2_fma(x[i][k], x[i][k], a);
+        }
+      }
+      q[i] = both(a);
     }
     group_sum(q, buf[1], tpr, g, t);
-    const float rstd = 1.0f / sqrtf(q[0] * inv + p.eps);
-    if (!kKeep) {
-      load_params<P, VEC, NV>(w, p.weight, 1.f, t, tpr, nv);
-      load_params<P, VEC, NV>(b, p.bias, 0.f, t, tpr, nv);
-    }
-    T* y = static_cast<T*>(p.y) + r * p.ldy;
+    f32x2 rr[R];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      float v[VEC];
+    for (int i = 0; i < R; ++i) {
+      const float rstd = reciprocal_root(q[i] * inv + p.eps);
+      rr[i] = f2(rstd, rstd);
+      if (r + i < p.rows && t == 0) {
+        p.mean[r + i] = s[i];
+        p.rstd[r + i] = rstd;
+      }
+    }
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) v[i] = fmaf(x[j * VEC + i] * rstd, w[j * VEC + i], b[j * VEC + i]);
-      if (ok && j < nv) store<T, VEC>(y, (t + j * tpr) * VEC, v);
+    for (int k = 0; k < E / 4; ++k) {
+      f32x2 w[2], b[2];
+      if constexpr (RING) {
+        read_params(wsm, k, tpr, t, w[0], w[1]);
+        read_params(bsm, k, tpr, t, b[0], b[1]);
+      } else {
+        w[0] = wreg[2 * k], w[1] = wreg[2 * k + 1];
+        b[0] = breg[2 * k], b[1] = breg[2 * k + 1];
+      }
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) x[i][2 * k + h] = f2_fma(f2_mul(x[i][2 * k + h], rr[i]), w[h], b[h]);
     }
-    if (ok && t == 0) {
-      p.mean[r] = mean;
-      p.rstd[r] = rstd;
-    }
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (r + i < p.rows) store_row<T, VEC, NV>(static_cast<T*>(p.y) + (r + i) * p.ldy, t, tpr, nv, x[i]);
   }
+  if (RING) ring_wait(0);
 }
 
 // SUMS: each thread also adds up its columns' dy xhat and dy over the rows of
 // its group; the block's groups are added in their order at the end and the
-// block writes one partial.
-template <typename T, typename P, int VEC, int NV, bool SUMS>
-__global__ void __launch_bounds__(SUMS ? kBwdThreads : kFwdThreads) backward_kernel(const BwdParams p, int tpr, int groups) {
+// block writes one partial.  Values beyond the row are zeros of dy, so they
+// add nothing; rows beyond the matrix have rstd 0.
+template <typename T, typename P, int VEC, int NV, bool SUMS, bool RING>
+__global__ void __launch_bounds__(SUMS ? kBwdThreads : kFwdThreads) backward_kernel(const BwdParams p, int tpr, int groups, int depth) {
   constexpr int E = VEC * NV;
   __shared__ float buf[2][2][32];
-  extern __shared__ float part[];  // SUMS: groups * tpr * E
+  extern __shared__ __align__(16) uint8_t smem[];
   const int g = threadIdx.x / tpr, t = threadIdx.x - g * tpr;
   const long long step = static_cast<long long>(gridDim.x) * groups;
   const int nv = max(0, (p.cols - t * VEC + tpr * VEC - 1) / (tpr * VEC));
-  constexpr bool kKeep = E <= 8;
-  constexpr bool kAhead = VEC > 1;
-  float w[E], dw[SUMS ? E : 1], db[SUMS ? E : 1];
-  if (kKeep) load_params<P, VEC, NV>(w, p.weight, 1.f, t, tpr, nv);
+  const float inv = 1.0f / p.cols;
+  const T* x0 = static_cast<const T*>(p.x) + (nv ? t * VEC : 0);
+  const T* g0 = static_cast<const T*>(p.dy) + (nv ? t * VEC : 0);
+  const Ring<T, VEC, NV> rx(smem_u32(smem), blockDim.x, nv);
+  const Ring<T, VEC, NV> rg(smem_u32(smem) + depth * blockDim.x * rx.kRow, blockDim.x, nv);
+  float* wsm = reinterpret_cast<float*>(smem + static_cast<size_t>(depth) * 2 * blockDim.x * rx.kRow);
+  const long long first = static_cast<long long>(blockIdx.x) * groups;
+  long long ahead = first + g;
+  int head = 0;
+  float nmean = 0.f, nrstd = 0.f;  // the next row's
+  if (ahead < p.rows) {
+    nmean = p.mean[ahead];
+    nrstd = p.rstd[ahead];
+  }
+  auto start = [&] {
+    const bool in = ahead < p.rows;
+    rx.start(head, in ? x0 + ahead * p.ldx : x0, tpr, in);
+    rg.start(head, in ? g0 + ahead * p.lddy : g0, tpr, in);
+    ring_commit();
+    ahead += step;
+    if (++head == depth) head = 0;
+  };
+  if constexpr (RING) {
+    for (int i = 1; i < depth; ++i) start();
+    stage_params<P, VEC, NV>(wsm, p.weight, 1.f, tpr, p.cols);
+    __syncthreads();
+  }
+  f32x2 dw[SUMS ? E / 2 : 1], db[SUMS ? E / 2 : 1];
   if (SUMS)
 #pragma unroll
-    for (int k = 0; k < E; ++k) dw[k] = db[k] = 0.f;
-  const float inv = 1.0f / p.cols;
-  Held<T, VEC, NV> nx, ng;
-  float nmean = 0.f, nrstd = 0.f;
-  auto fetch = [&](long long r) {
-    const bool ok = r < p.rows;
-    nx.load(static_cast<const T*>(p.x) + r * p.ldx, t, tpr, ok ? nv : 0);
-    ng.load(static_cast<const T*>(p.dy) + r * p.lddy, t, tpr, ok ? nv : 0);
-    nmean = ok ? p.mean[r] : 0.f;
-    nrstd = ok ? p.rstd[r] : 0.f;
-  };
-  if (kAhead) fetch(static_cast<long long>(blockIdx.x) * groups + g);
-  int turn = 0;
-  for (long long base = static_cast<long long>(blockIdx.x) * groups; base < p.rows; base += step) {
+    for (int k = 0; k < E / 2; ++k) dw[k] = db[k] = f2(0.f, 0.f);
+  int turn = 0, slot = 0;
+  for (long long base = first; base < p.rows; base += step) {
     const long long r = base + g;
     const bool ok = r < p.rows;
-    if (!kAhead) fetch(r);
-    const float mean = nmean, rstd = nrstd;
-    float xhat[E], d[E];
-    if (!kKeep) load_params<P, VEC, NV>(w, p.weight, 1.f, t, tpr, nv);
-    float s[2] = {0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < E; ++k) {
-      xhat[k] = k / VEC < nv ? (nx.get(k) - mean) * rstd : 0.f;
-      d[k] = ng.get(k);
-      if (SUMS) {
-        dw[k] = fmaf(d[k], xhat[k], dw[k]);
-        db[k] += d[k];
-      }
-      d[k] *= w[k];
-      s[0] += d[k];
-      s[1] = fmaf(d[k], xhat[k], s[1]);
+    f32x2 xhat[E / 2], d[E / 2], wreg[RING ? 1 : E / 2];
+    Held<T, VEC, NV> hx, hg;
+    if constexpr (RING) {
+      start();
+    } else {
+      hx.load(x0 + (ok ? r * p.ldx : 0), tpr, ok ? nv : 0);
+      hg.load(g0 + (ok ? r * p.lddy : 0), tpr, ok ? nv : 0);
+      load_params<P, VEC, NV>(wreg, p.weight, 1.f, t, tpr, nv);
     }
-    if (kAhead) fetch(r + step);
+    const float rstd = ok ? nrstd : 0.f;
+    const f32x2 mean = f2(nmean, nmean), rr = f2(rstd, rstd);
+    const long long rn = r + step < p.rows ? r + step : 0;
+    nmean = p.mean[rn];
+    nrstd = p.rstd[rn];
+    if constexpr (RING) {
+      ring_wait(depth - 1);
+      rx.read(slot, xhat);
+      rg.read(slot, d);
+      if (++slot == depth) slot = 0;
+    } else {
+      hx.read(xhat);
+      hg.read(d);
+    }
+    f32x2 a = f2(0.f, 0.f), c = f2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < E / 4; ++k) {
+      f32x2 w[2];
+      if constexpr (RING)
+        read_params(wsm, k, tpr, t, w[0], w[1]);
+      else
+        w[0] = wreg[2 * k], w[1] = wreg[2 * k + 1];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i = 2 * k + h;
+        xhat[i] = f2_mul(f2_sub(xhat[i], mean), rr);
+        if (SUMS) {
+          dw[i] = f2_fma(d[i], xhat[i], dw[i]);
+          db[i] = f2_add(db[i], d[i]);
+        }
+        d[i] = f2_mul(d[i], w[h]);
+        a = f2_add(a, d[i]);
+        c = f2_fma(d[i], xhat[i], c);
+      }
+    }
+    float s[2] = {both(a), both(c)};
     group_sum(s, buf[turn], tpr, g, t);
     turn ^= 1;
-    const float m = s[0] * inv, q = s[1] * inv;
-    T* dx = static_cast<T*>(p.dx) + r * p.lddx;
+    const f32x2 m = f2(s[0] * inv, s[0] * inv), q = f2(-s[1] * inv, -s[1] * inv);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      float v[VEC];
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const int k = j * VEC + i;
-        v[i] = rstd * (d[k] - m - xhat[k] * q);
-      }
-      if (ok && j < nv) store<T, VEC>(dx, (t + j * tpr) * VEC, v);
-    }
+    for (int k = 0; k < E / 2; ++k) d[k] = f2_mul(rr, f2_fma(xhat[k], q, f2_sub(d[k], m)));
+    if (ok) store_row<T, VEC, NV>(static_cast<T*>(p.dx) + r * p.lddx, t, tpr, nv, d);
   }
+  if (RING) ring_wait(0);
   if (SUMS && p.parts) {
+    float* part = reinterpret_cast<float*>(smem);  // groups * tpr * E; the ring is done with
     float* out = p.partials + static_cast<long long>(blockIdx.x) * 2 * p.cols;
     const int span = tpr * E;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const float* mine = h ? db : dw;
       __syncthreads();
 #pragma unroll
-      for (int k = 0; k < E; ++k) part[g * span + (t + (k / VEC) * tpr) * VEC + k % VEC] = mine[k];
+      for (int k = 0; k < E / 2; ++k) {
+        float lo, hi;
+        f2_split(h ? db[k] : dw[k], lo, hi);
+        part[g * span + (t + (2 * k / VEC) * tpr) * VEC + 2 * k % VEC] = lo;
+        part[g * span + (t + ((2 * k + 1) / VEC) * tpr) * VEC + (2 * k + 1) % VEC] = hi;
+      }
       __syncthreads();
       for (int c = threadIdx.x; c < p.cols; c += blockDim.x) {
         float v = part[c];
@@ -464,22 +722,43 @@ Shape shape_of(long long rows, int cols, int sms, int max_e, int max_threads) {
   return s;
 }
 
-// Resident blocks of a kernel (registers bound it) at this block size.
-template <typename K>
-int blocks_per_sm(K kernel, int threads, size_t smem) {
-  static thread_local int device = -1, cached_threads = 0, cached = 0;
-  static thread_local size_t cached_smem = 0;
+// Ring slots of a block, its shared memory, and its resident blocks an SM:
+// asked once for a kernel and block.
+struct Fit {
+  int depth, smem, blocks;
+};
+
+template <auto kernel>
+cudaError_t fit_of(int threads, int slot_bytes, int other_bytes, int least_bytes, Fit* fit) {
+  static thread_local int device = -1, was_threads = 0, was_slot = 0, was_other = 0;
+  static thread_local Fit was;
   int dev = 0;
   cudaGetDevice(&dev);
-  if (dev != device || threads != cached_threads || smem != cached_smem) {
+  if (dev != device || threads != was_threads || slot_bytes != was_slot || other_bytes != was_other) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget);
+    if (e != cudaSuccess) return e;
     int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess || n < 1) n = 1;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0);  // by registers and threads
+    if (e != cudaSuccess) return e;
+    if (n < 1) return cudaErrorInvalidConfiguration;
+    while (n > 1 && kSmemBudget / n < other_bytes + 3 * slot_bytes) --n;
+    Fit f;
+    f.depth = slot_bytes ? (kSmemBudget / n - other_bytes) / slot_bytes : 1;
+    if (f.depth > kMaxDepth) f.depth = kMaxDepth;
+    if (f.depth < 1) return cudaErrorInvalidConfiguration;
+    f.smem = f.depth * slot_bytes + other_bytes;
+    if (f.smem < least_bytes) f.smem = least_bytes;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&f.blocks, kernel, threads, f.smem);
+    if (e != cudaSuccess) return e;
+    if (f.blocks < 1) return cudaErrorInvalidConfiguration;
+    was = f;
     device = dev;
-    cached_threads = threads;
-    cached_smem = smem;
-    cached = n;
+    was_threads = threads;
+    was_slot = slot_bytes;
+    was_other = other_bytes;
   }
-  return cached;
+  *fit = was;
+  return cudaSuccess;
 }
 
 bool aligned(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -489,21 +768,34 @@ bool aligned_rows(const void* p, long long ld, long long rows) {
   return aligned(p) && (rows <= 1 || ld * sizeof(T) % 16 == 0);
 }
 
+template <typename T, typename P, int VEC, int NV, int R, bool RING>
+cudaError_t forward_with(const FwdParams& p, const Shape& h, int sms, cudaStream_t s) {
+  const int threads = h.tpr * h.groups;
+  Fit f;
+  const cudaError_t e = fit_of<forward_kernel<T, P, VEC, NV, R, RING>>(
+      threads, RING ? threads * R * Ring<T, VEC, NV>::kRow : 0, RING ? 2 * VEC * NV * h.tpr * 4 : 0, 0, &f);
+  if (e != cudaSuccess) return e;
+  const long long want = (p.rows + h.groups * R - 1) / (h.groups * R), most = static_cast<long long>(sms) * f.blocks;
+  forward_kernel<T, P, VEC, NV, R, RING>
+      <<<static_cast<int>(want < most ? want : most), threads, f.smem, s>>>(p, h.tpr, h.groups, f.depth);
+  return cudaGetLastError();
+}
+
+// Rows enough for the ring: four or more a group.
+bool many_rows(long long rows, const Shape& h, int sms) { return rows >= 4ll * sms * h.groups; }
+
 template <typename T, typename P, int VEC, int NV>
 cudaError_t forward_as(const FwdParams& p, const Shape& h, int sms, cudaStream_t s) {
-  const int threads = h.tpr * h.groups;
-  const long long want = (p.rows + h.groups - 1) / h.groups;
-  long long most = sms;
-  if (want > most) most = static_cast<long long>(sms) * blocks_per_sm(forward_kernel<T, P, VEC, NV>, threads, 0);
-  forward_kernel<T, P, VEC, NV><<<static_cast<int>(want < most ? want : most), threads, 0, s>>>(p, h.tpr, h.groups);
-  return cudaGetLastError();
+  constexpr int R = VEC > 1 && VEC * NV <= 24 ? 2 : 1;  // rows a group of the ring holds at once
+  if constexpr (VEC > 1 || sizeof(T) == 4)
+    if (many_rows(p.rows, h, sms)) return forward_with<T, P, VEC, NV, R, true>(p, h, sms, s);
+  return forward_with<T, P, VEC, NV, 1, false>(p, h, sms, s);
 }
 
 template <typename T, typename P>
 cudaError_t forward(const FwdParams& p, int sms, cudaStream_t s) {
   constexpr int V = 16 / static_cast<int>(sizeof(T));
-  const bool vec = p.cols % V == 0 && aligned_rows<T>(p.x, p.ldx, p.rows) && aligned_rows<T>(p.y, p.ldy, p.rows) &&
-                   aligned(p.weight) && aligned(p.bias);
+  const bool vec = p.cols % V == 0 && aligned_rows<T>(p.x, p.ldx, p.rows) && aligned_rows<T>(p.y, p.ldy, p.rows);
   const Shape h = shape_of(p.rows, p.cols, sms, vec || p.cols > kFwdE / 2 * kFwdThreads ? kFwdE : kFwdE / 2, kFwdThreads);
   switch (h.e) {
     case 8: return vec ? forward_as<T, P, V, 8 / V>(p, h, sms, s) : forward_as<T, P, 1, 8>(p, h, sms, s);
@@ -524,27 +816,50 @@ int column_blocks(long long rows, const Shape& h, int sms) {
   return static_cast<int>(want < most ? want : most);
 }
 
-template <typename T, typename P, int VEC, int NV, bool SUMS>
-cudaError_t backward_as(const BwdParams& p, const Shape& h, int sms, cudaStream_t s) {
+// One-value accesses leave fewer registers: 16 values a thread where they hold the row.
+Shape backward_shape(long long rows, int cols, int sms, bool vec) {
+  return shape_of(rows, cols, sms, vec || cols > 16 * kBwdThreads ? kBwdE : 16, kBwdThreads);
+}
+
+// Runs of rows of column_kernel: at least 64 rows, 64 of them at most.
+int column_runs(long long rows) {
+  const long long n = (rows + 63) / 64;
+  return static_cast<int>(n < 64 ? n : 64);
+}
+
+template <typename T, typename P, int VEC, int NV, bool SUMS, bool RING>
+cudaError_t backward_with(const BwdParams& p, const Shape& h, int sms, cudaStream_t s) {
   const int threads = h.tpr * h.groups;
-  const size_t smem = SUMS ? static_cast<size_t>(threads) * VEC * NV * 4 : 0;  // 36 KiB at most
+  Fit f;
+  const cudaError_t e = fit_of<backward_kernel<T, P, VEC, NV, SUMS, RING>>(
+      threads, RING ? threads * 2 * Ring<T, VEC, NV>::kRow : 0, RING ? VEC * NV * h.tpr * 4 : 0,
+      SUMS ? threads * VEC * NV * 4 : 0, &f);
+  if (e != cudaSuccess) return e;
   long long blocks = SUMS ? column_blocks(p.rows, h, sms) : p.rows;
-  if (!SUMS && blocks > sms) blocks = sms;
-  backward_kernel<T, P, VEC, NV, SUMS><<<static_cast<int>(blocks), threads, smem, s>>>(p, h.tpr, h.groups);
+  if (!SUMS && blocks > static_cast<long long>(sms) * f.blocks) blocks = static_cast<long long>(sms) * f.blocks;
+  backward_kernel<T, P, VEC, NV, SUMS, RING><<<static_cast<int>(blocks), threads, f.smem, s>>>(p, h.tpr, h.groups, f.depth);
   return cudaGetLastError();
 }
 
+template <typename T, typename P, int VEC, int NV, bool SUMS>
+cudaError_t backward_as(const BwdParams& p, const Shape& h, int sms, cudaStream_t s) {
+  if constexpr (VEC > 1)
+    if (many_rows(p.rows, h, sms)) return backward_with<T, P, VEC, NV, SUMS, true>(p, h, sms, s);
+  return backward_with<T, P, VEC, NV, SUMS, false>(p, h, sms, s);
+}
+
 template <typename T, typename P>
-cudaError_t backward(const BwdParams& p, int sms, cudaStream_t s) {
+cudaError_t backward(BwdParams p, int sms, cudaStream_t s) {
   constexpr int V = 16 / static_cast<int>(sizeof(T));
-  Shape h = shape_of(p.rows, p.cols, sms, kBwdE, kBwdThreads);
+  const bool vec = p.cols % V == 0 && aligned_rows<T>(p.x, p.ldx, p.rows) && aligned_rows<T>(p.dy, p.lddy, p.rows) &&
+                   aligned_rows<T>(p.dx, p.lddx, p.rows);
+  Shape h = backward_shape(p.rows, p.cols, sms, vec);
   const bool held = h.e != 0;  // rows whose columns are added up on the way
+  if (p.parts) p.parts = held ? column_blocks(p.rows, h, sms) : column_runs(p.rows);
   if (!held) {
     h = shape_of(p.rows, p.cols, sms, kFwdE, kFwdThreads);
     h.groups = 1;
   }
-  const bool vec = p.cols % V == 0 && aligned_rows<T>(p.x, p.ldx, p.rows) && aligned_rows<T>(p.dy, p.lddy, p.rows) &&
-                   aligned_rows<T>(p.dx, p.lddx, p.rows) && aligned(p.weight);
   cudaError_t e = cudaSuccess;
   if (p.rows > 0) {
     if (held && h.e == 8)
@@ -571,13 +886,16 @@ cudaError_t backward(const BwdParams& p, int sms, cudaStream_t s) {
 
 }  // namespace
 
-// One partial a block where the columns are added up with the rows held in
-// registers; for wider rows runs of at least 64 rows, 64 of them at most.
+// The most that either access width needs: one partial a block where the
+// columns are added up on the way, else one a run of rows.
 int partial_count(long long rows, int cols, int sms) {
-  const Shape h = shape_of(rows, cols, sms, kBwdE, kBwdThreads);
-  if (h.e) return column_blocks(rows, h, sms);
-  const long long n = (rows + 63) / 64;
-  return static_cast<int>(n < 64 ? n : 64);
+  int most = 0;
+  for (const bool vec : {false, true}) {
+    const Shape h = backward_shape(rows, cols, sms, vec);
+    const int n = h.e ? column_blocks(rows, h, sms) : column_runs(rows);
+    if (n > most) most = n;
+  }
+  return most;
 }
 
 cudaError_t launch_forward(const FwdParams& p, int dtype, int param_dtype, int sms, cudaStream_t s) {
