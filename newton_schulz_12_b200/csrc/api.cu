@@ -1326,18 +1326,19 @@ int workspace_status(cudaStream_t s, int** status) {
 
 unsigned long long wait_timeout_ns() { return g_timeout_ns; }
 
-int encode_bytes_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint64_t stride,
-                    uint32_t box_inner, uint32_t box_rows) {
+int encode_2d(CUtensorMap* map, const void* base, bool words, uint64_t inner, uint64_t rows, uint64_t stride_bytes,
+              uint32_t box_inner, uint32_t box_rows) {
   MUON_TRY(get_encoder());
   cuuint64_t dims[2] = {inner, rows};
-  cuuint64_t strides[1] = {stride};
+  cuuint64_t strides[1] = {stride_bytes};
   cuuint32_t box[2] = {box_inner, box_rows};
   cuuint32_t es[2] = {1, 1};
-  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  const CUresult r = g_encode(map, words ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+                              const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              words ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS)
-    return set_err(MUON_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for %llu bytes x %llu rows, box %ux%u",
+    return set_err(MUON_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for %llu x %llu rows, box %ux%u",
                    static_cast<int>(r), (unsigned long long)inner, (unsigned long long)rows, box_inner, box_rows);
   return MUON_OK;
 }

@@ -325,8 +325,14 @@ int product_impl(long long m, long long n, long long k, const void* a_data, cons
   p.a_scales = p.transposed ? b_scales : a_scales;
   p.b_scales = p.transposed ? a_scales : b_scales;
   const uint64_t row = static_cast<uint64_t>(mx::data_stride(k));
-  TRY(host::encode_bytes_2d(&p.a, p.transposed ? b_data : a_data, row, p.m, row, 128, 128));
-  TRY(host::encode_bytes_2d(&p.b, p.transposed ? a_data : b_data, row, p.n, row, 128, mx::product_tile_n(p.m, p.n)));
+  const int tile_n = mx::product_tile_n(p.m, p.n, sms);
+  TRY(host::encode_2d(&p.a, p.transposed ? b_data : a_data, false, row, p.m, row, 128, 128));
+  TRY(host::encode_2d(&p.b, p.transposed ? a_data : b_data, false, row, p.n, row, 128, tile_n == 256 ? 128 : tile_n));
+  if (tile_n == 256) {
+    const uint64_t words = static_cast<uint64_t>(tile_count(k)) * 128;
+    TRY(host::encode_2d(&p.sa, p.a_scales, true, words, tile_count(p.m), words * 4, 256, 1));
+    TRY(host::encode_2d(&p.sb, p.b_scales, true, words, tile_count(p.n), words * 4, 256, 2));
+  }
   host::Timed timed(MUON_KERNEL_MX_PRODUCT, s);
   TRY_CUDA(mx::launch_product(p, dtype, sms, s));
   return MUON_OK;

@@ -433,6 +433,7 @@ cudaError_t launch_dequantize(const DequantParams& p, int dtype, int sms, cudaSt
 // C = A B^T, A m x k and B n x k in 4 bits.
 struct ProductParams {
   CUtensorMap a, b;      // data, bytes, 128-byte swizzle
+  CUtensorMap sa, sb;    // scales, 4-byte words, a tile row each (only for tiles of 256 columns)
   const void* a_scales;
   const void* b_scales;
   void* out;
@@ -443,8 +444,9 @@ struct ProductParams {
   unsigned long long timeout_ns;
 };
 
-// Rows of the tile that the b map's box has to cover for an m x n product.
-int product_tile_n(int m, int n);
+// Columns of the tiles of an m x n product, m >= n where n <= 64: b's box has as
+// many rows, or half as many for tiles of 256 (a pair of CTAs).
+int product_tile_n(int m, int n, int sms);
 cudaError_t launch_product(const ProductParams& p, int dtype, int sms, cudaStream_t s);
 // Reads and clears the current device's status word of captured launches.
 cudaError_t take_captured_status(int* value);
@@ -459,8 +461,9 @@ void clear_error();
 int device_sms(int* sms);                       // checks the device, too
 int workspace_status(cudaStream_t s, int** status);  // device status word of (current device, stream)
 unsigned long long wait_timeout_ns();
-int encode_bytes_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint64_t stride,
-                    uint32_t box_inner, uint32_t box_rows);
+// A 2-D map of bytes with 128-byte swizzle (`words` false) or of 4-byte words without.
+int encode_2d(CUtensorMap* map, const void* base, bool words, uint64_t inner, uint64_t rows, uint64_t stride_bytes,
+              uint32_t box_inner, uint32_t box_rows);
 
 // Brackets one launch with events while kernel timing is on.
 class Timed {

@@ -91,6 +91,33 @@ __device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uin
       : "memory");
 }
 
+// Pair forms: the box lands in this CTA's shared memory and is credited to the
+// barrier `cbar` of the pair's leader; a copy of scales runs in both CTAs, each
+// from its own shared memory; a product takes 128 rows of A and half of B's rows
+// from each CTA.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* map, uint32_t cbar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(cbar), "r"(c0), "r"(c1)
+      : "memory");
+}
+__device__ __forceinline__ void scales_to_tmem_pair(uint32_t taddr, uint32_t saddr) {
+  uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(128u >> 4) << 32;
+  d |= 1ull << 46;
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+__device__ __forceinline__ void mma_mxf4_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+      : "memory");
+}
+
 template <typename T>
 __device__ __forceinline__ T rounded(float v);
 template <>
@@ -99,6 +126,29 @@ template <>
 __device__ __forceinline__ bf16 rounded<bf16>(float v) { return __float2bfloat16_rn(v); }
 template <>
 __device__ __forceinline__ __half rounded<__half>(float v) { return __float2half_rn(v); }
+
+// A warp's 32 rows x CW columns from their staging rows to C, cut at its edges.
+template <typename T, int CW>
+__device__ __forceinline__ void store_chunk(T* out, const ProductParams& p, const uint8_t* stg, uint32_t stg_row, long long row0,
+                                            long long col0, int lane, bool vec) {
+  constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+  if (vec && col0 + CW <= p.n) {
+    constexpr int per_row = CW / kVec;
+#pragma unroll
+    for (int e = lane; e < 32 * per_row; e += 32) {
+      const int r = e / per_row, u = e % per_row;
+      if (row0 + r < p.m)
+        *reinterpret_cast<uint4*>(out + (row0 + r) * p.ldo + col0 + u * kVec) =
+            *reinterpret_cast<const uint4*>(stg + r * stg_row + u * 16);
+    }
+  } else {
+    for (int e = lane; e < 32 * CW; e += 32) {
+      const int r = e / CW, c = e % CW;
+      if (row0 + r < p.m && col0 + c < p.n)
+        out[(row0 + r) * p.ldo + col0 + c] = reinterpret_cast<const T*>(stg + r * stg_row)[c];
+    }
+  }
+}
 
 template <int BN, typename T, bool TRANS>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ ProductParams p) {
@@ -292,21 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         }
         if (!TRANS) {
           __syncwarp();
-          if (vec && col0 + CW <= p.n) {
-            constexpr int per_row = CW / kVec;
-            for (int e = lane; e < 32 * per_row; e += 32) {
-              const int r = e / per_row, u = e % per_row;
-              if (row0 + r < p.m)
-                *reinterpret_cast<uint4*>(out + (row0 + r) * p.ldo + col0 + u * kVec) =
-                    *reinterpret_cast<const uint4*>(stg + r * C::kStageRow + u * 16);
-            }
-          } else {
-            for (int e = lane; e < 32 * CW; e += 32) {
-              const int r = e / CW, c = e % CW;
-              if (row0 + r < p.m && col0 + c < p.n)
-                out[(row0 + r) * p.ldo + col0 + c] = reinterpret_cast<const T*>(stg + r * C::kStageRow)[c];
-            }
-          }
+          store_chunk<T, CW>(out, p, stg, C::kStageRow, row0, col0, lane, vec);
           __syncwarp();
         }
       }
@@ -327,6 +363,283 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   }
 }
 
+// ---------------------------------------------------------------------------
+// Large products: a pair of CTAs holds a 256 x 256 tile of C (128 rows each), so
+// that each SM reads half of B's tile from its shared memory and 8 KiB feed a
+// step of 128 cycles.  Two accumulators of 256 columns and two slots of scales
+// do not fit the 512 columns of tensor memory side by side: the accumulators
+// share 48 columns, which the epilogue reads first, and the next tile starts
+// once they are read.
+// ---------------------------------------------------------------------------
+namespace pair {
+
+constexpr int BN = 256;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr uint32_t kABytes = BM * 128, kBBytes = BN / 2 * 128;
+constexpr uint32_t kScaleA = 2 * kScaleTile, kScaleB = 4 * kScaleTile;  // a stage: two tiles along k; B's 256 rows in both CTAs
+constexpr uint32_t kStageBytes = kABytes + kBBytes + kScaleA + kScaleB;
+constexpr uint32_t kSlotCols = 8 + 16;
+constexpr uint32_t kScaleCol = 512 - 2 * kSlotCols;
+constexpr uint32_t kAcc1 = kScaleCol - BN;  // 208: columns 208 .. 255 are shared
+constexpr int kChunk = 64;
+static_assert(BN - kAcc1 <= kChunk, "the shared columns lie in one chunk");
+
+template <typename T>
+struct Cfg {
+  static constexpr int kStages = sizeof(T) == 4 ? 4 : 5;
+  static constexpr uint32_t kRow = kChunk * sizeof(T) + 16;  // staging row, padded against bank conflicts
+  static constexpr int kBars = 2 * kStages + 6;              // full, empty; tfull x 2; early; scale slots x 2; drain
+  static constexpr size_t kSmem = 1024 + kStages * kStageBytes + kEpiWarps * 32 * kRow + kBars * 8 + 16;
+  static_assert(kSmem <= 232448, "shared memory");
+};
+
+// Tile t of the launch: runs of 8 tile rows, column by column, so that tiles
+// that run together share operands in L2.
+__device__ __forceinline__ void tile_of(int t, int tiles_m, int tiles_n, int& tm, int& tn) {
+  const int run = 8 * tiles_n, r = t / run, rest = t - r * run;
+  const int rows = min(8, tiles_m - 8 * r);
+  tn = rest / rows;
+  tm = 8 * r + rest - tn * rows;
+}
+
+template <typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    pair_kernel(const __grid_constant__ ProductParams p) {
+  using C = Cfg<T>;
+  constexpr int S = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* staging = smem + S * kStageBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + kEpiWarps * 32 * C::kRow);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::kBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const uint32_t peer = static_cast<uint32_t>(rank ^ 1);
+  const int first = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const uint32_t bar0 = smem_u32(bars), smem0 = smem_u32(smem);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (S + s); };
+  auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * S + a); };
+  const uint32_t early_bar = bar0 + 8u * (2 * S + 2);
+  auto slot_bar = [&](int a) { return bar0 + 8u * (2 * S + 3 + a); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * S + 5);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(slot_bar(a), 1);
+    }
+    mbar_init(early_bar, 2 * kEpiWarps);  // the leader's: the epilogue warps of both CTAs
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_holder), 512);
+    tmem_relinquish_pair();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_map(&p.a);
+    tma_prefetch_map(&p.b);
+    tma_prefetch_map(&p.sa);
+    tma_prefetch_map(&p.sb);
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+
+  WaitCtl ctl;
+  ctl.abort_flag = abort_flag;
+  ctl.status = p.status ? p.status : &g_captured_status;
+  ctl.timeout_ns = p.timeout_ns;
+  ctl.where = 0;
+  ctl.peer_abort = cluster_addr(smem_u32(const_cast<int*>(abort_flag)), peer);
+  const unsigned long long drain_ns = p.timeout_ns < 50000000ull ? p.timeout_ns : 50000000ull;
+
+  const int tiles_m = (p.m + 2 * BM - 1) / (2 * BM), tiles_n = (p.n + BN - 1) / BN;
+  const int tiles = tiles_m * tiles_n;
+  const int kiters = (p.k + kStageK - 1) / kStageK;
+
+  if (warp == 0) {
+    // copies, in both CTAs
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, parity = 0;
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += npairs) {
+        int tm, tn;
+        tile_of(t, tiles_m, tiles_n, tm, tn);
+        for (int it = 0; it < kiters; ++it) {
+          if (!mbar_wait(empty_bar(stage), phase ^ 1u, ctl)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fbar = cluster_addr(full_bar(stage), 0);
+          if (rank == 0) {
+            mbar_arrive_expect_tx(full_bar(stage), 2 * kStageBytes);  // what lies beyond a matrix comes as zeros and counts
+            issued |= 1u << stage;
+            parity = (parity & ~(1u << stage)) | (phase << stage);
+          }
+          const uint32_t a = smem0 + stage * kStageBytes, b = a + kABytes, sa = b + kBBytes, sb = sa + kScaleA;
+          tma_load_2d_pair(a, &p.a, fbar, it * 128, (2 * tm + rank) * BM);
+          tma_load_2d_pair(b, &p.b, fbar, it * 128, tn * BN + rank * (BN / 2));
+          tma_load_2d_pair(sa, &p.sa, fbar, it * 256, 2 * tm + rank);
+          tma_load_2d_pair(sb, &p.sb, fbar, it * 256, 2 * tn);
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok)
+        for (int s = 0; s < S; ++s)
+          if (issued & (1u << s)) mbar_wait_drain(full_bar(s), (parity >> s) & 1u, drain_ns);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      int stage = 0, slot = 0;
+      uint32_t phase = 0, slot_phase = 0;
+      bool ok = true;
+      for (int t = first, k = 0; t < tiles && ok; t += npairs, ++k) {
+        // the tile before last is read out and the shared columns of the last one too
+        if (k > 0 && !mbar_wait(early_bar, static_cast<uint32_t>(k - 1) & 1u, ctl)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + (k & 1 ? kAcc1 : 0u);
+        for (int it = 0; it < kiters; ++it) {
+          // the slot's scales were last read by the products of two stages ago
+          if (!mbar_wait(full_bar(stage), phase, ctl) || !mbar_wait(slot_bar(slot), slot_phase ^ 1u, ctl)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = smem0 + stage * kStageBytes, b = a + kABytes, sa = b + kBBytes, sb = sa + kScaleA;
+          const uint32_t ta = tmem + kScaleCol + static_cast<uint32_t>(slot) * kSlotCols, tb = ta + 8;
+          const int steps = min(4, (p.k - it * kStageK + 63) / 64);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (2 * h >= steps) break;
+            scales_to_tmem_pair(ta + 4 * h, sa + h * kScaleTile);
+            scales_to_tmem_pair(tb + 8 * h, sb + h * kScaleTile);
+            scales_to_tmem_pair(tb + 8 * h + 4, sb + (2 + h) * kScaleTile);
+          }
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            if (kk >= steps) break;
+            const uint32_t h = kk >> 1;
+            mma_mxf4_pair(d, sdesc_sw128(a + kk * 32, 16, 1024), sdesc_sw128(b + kk * 32, 16, 1024),
+                          idesc_mxf4(2 * BM, BN, 2 * (kk & 1)), ta + 4 * h, tb + 8 * h, (it | kk) != 0 ? 1u : 0u);
+          }
+          tc_commit_pair(empty_bar(stage));
+          tc_commit_pair(cluster_addr(empty_bar(stage), peer));
+          tc_commit_pair(slot_bar(slot));
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          if (++slot == 2) {
+            slot = 0;
+            slot_phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        tc_commit_pair(tfull_bar(k & 1));
+        tc_commit_pair(cluster_addr(tfull_bar(k & 1), peer));
+      }
+      tc_commit_pair(drain_bar);
+      mbar_wait_drain(drain_bar, 0, drain_ns > 1000000ull ? drain_ns : 1000000ull);
+    }
+    __syncwarp();
+  } else {
+    // two warps a lane quarter, alternate chunks; the one with the shared columns first
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    constexpr uint32_t kRow = C::kRow;
+    uint8_t* stg = staging + (warp - 2) * 32 * kRow;
+    T* out = static_cast<T*>(p.out);
+    constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+    const bool vec = (reinterpret_cast<uintptr_t>(out) % 16 == 0) && (p.ldo % kVec == 0);
+    const uint32_t early = cluster_addr(early_bar, 0);
+    for (int t = first, k = 0; t < tiles; t += npairs, ++k) {
+      int tm, tn;
+      tile_of(t, tiles_m, tiles_n, tm, tn);
+      const bool ok = mbar_wait(tfull_bar(k & 1), (k >> 1) & 1, ctl);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      tc_fence_after();
+      if (half == 1 && lane == 0) mbar_arrive_remote(early);  // this warp has left the tile before
+      const long long row0 = static_cast<long long>(2 * tm + rank) * BM + quarter * 32;
+#pragma unroll 1
+      for (int i = half; i < BN / kChunk; i += 2) {
+        const int c0 = (k & 1 ? i : BN / kChunk - 1 - i) * kChunk;
+        const long long col0 = static_cast<long long>(tn) * BN + c0;
+        uint32_t r[2][32];
+        const uint32_t ta = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + (k & 1 ? kAcc1 : 0u) + static_cast<uint32_t>(c0);
+        tmem_ld_32x32(ta, r[0]);
+        tmem_ld_32x32(ta + 32, r[1]);
+        tmem_ld_wait();
+        if (i == 0) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(early);
+        }
+        if (row0 >= p.m || col0 >= p.n) continue;
+        T* mine = reinterpret_cast<T*>(stg + lane * kRow);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < 32; j += kVec) {
+            T v[kVec];
+#pragma unroll
+            for (int q = 0; q < kVec; ++q) v[q] = rounded<T>(__uint_as_float(r[h][j + q]));
+            *reinterpret_cast<uint4*>(mine + 32 * h + j) = *reinterpret_cast<const uint4*>(v);
+          }
+        __syncwarp();
+        store_chunk<T, kChunk>(out, p, stg, kRow, row0, col0, lane, vec);
+        __syncwarp();
+      }
+    }
+  }
+  tc_fence_before();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+template <typename T>
+cudaError_t launch(const ProductParams& p, int sms, cudaStream_t s) {
+  static thread_local int configured_device = -1, resident = 0;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (configured_device != dev) {
+    cudaError_t e = cudaFuncSetAttribute(pair_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(Cfg<T>::kSmem));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(sms / 2 * 2, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = Cfg<T>::kSmem;
+    e = cudaOccupancyMaxActiveClusters(&resident, pair_kernel<T>, &cfg);
+    if (e != cudaSuccess) return e;
+    configured_device = dev;
+  }
+  const long long tiles = static_cast<long long>((p.m + 2 * BM - 1) / (2 * BM)) * ((p.n + BN - 1) / BN);
+  long long pairs = sms / 2;
+  if (resident > 0 && pairs > resident) pairs = resident;
+  if (pairs > tiles) pairs = tiles;
+  pair_kernel<T><<<static_cast<int>(2 * pairs), kThreads, Cfg<T>::kSmem, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace pair
+
 template <int BN, typename T, bool TRANS>
 cudaError_t launch_one(const ProductParams& p, int sms, cudaStream_t s) {
   static thread_local int configured_device = -1;
@@ -345,7 +658,8 @@ cudaError_t launch_one(const ProductParams& p, int sms, cudaStream_t s) {
 
 template <typename T>
 cudaError_t launch_typed(const ProductParams& p, int sms, cudaStream_t s) {
-  switch (product_tile_n(p.m, p.n)) {
+  switch (product_tile_n(p.m, p.n, sms)) {
+    case 256: return pair::launch<T>(p, sms, s);
     case 32: return p.transposed ? launch_one<32, T, true>(p, sms, s) : launch_one<32, T, false>(p, sms, s);
     case 64: return p.transposed ? launch_one<64, T, true>(p, sms, s) : launch_one<64, T, false>(p, sms, s);
     default: return launch_one<128, T, false>(p, sms, s);
@@ -354,10 +668,16 @@ cudaError_t launch_typed(const ProductParams& p, int sms, cudaStream_t s) {
 
 }  // namespace
 
-// m is the larger side where the smaller one has at most 64 rows.
-int product_tile_n(int m, int n) {
-  (void)m;
-  return n <= 32 ? 32 : n <= 64 ? 64 : 128;
+// 32 or 64 where the smaller side has so few rows.  Else 256 (pairs of CTAs) or
+// 128 (one), whichever needs less time for its waves of tiles: a step of 64
+// along k takes a pair 128 cycles, and a CTA with its own 128 x 128 tile about
+// 80 (its shared memory, read at 128 bytes a cycle, bounds it, not the products).
+int product_tile_n(int m, int n, int sms) {
+  if (n <= 64) return n <= 32 ? 32 : 64;
+  auto waves = [](long long tiles, long long at_once) { return (tiles + at_once - 1) / at_once; };
+  const long long pairs = waves(static_cast<long long>((m + 255) / 256) * ((n + 255) / 256), sms / 2);
+  const long long single = waves(static_cast<long long>((m + 127) / 128) * ((n + 127) / 128), sms);
+  return pairs * 128 <= single * 80 ? 256 : 128;
 }
 
 cudaError_t launch_product(const ProductParams& p, int dtype, int sms, cudaStream_t s) {
