@@ -102,19 +102,43 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* map, 
       "l"(reinterpret_cast<uint64_t>(map)), "r"(cbar), "r"(c0), "r"(c1)
       : "memory");
 }
-__device__ __forceinline__ void scales_to_tmem_pair(uint32_t taddr, uint32_t saddr) {
-  uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(128u >> 4) << 32;
-  d |= 1ull << 46;
-  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+// Descriptors as two words: only the low one (the address) changes in the issue loop.
+constexpr uint32_t kOperandHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // 8-row groups 1 KiB apart, 128-byte swizzle
+constexpr uint32_t kOperandLo = 1u << 16;
+constexpr uint32_t kScaleHi = (128u >> 4) | (1u << 14);                  // 8-row groups of 16-byte rows, no swizzle
+__device__ __forceinline__ void scales_to_tmem_pair(uint32_t taddr, uint32_t lo) {
+  asm volatile(
+      "{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
+      "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr), "r"(lo), "r"(kScaleHi)
+      : "memory");
 }
-__device__ __forceinline__ void mma_mxf4_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
-                                              uint32_t accumulate) {
+template <int ID>
+__device__ __forceinline__ void mma_mxf4_pair(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t sa, uint32_t sb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "mov.b64 a, {%1, %7};\n\tmov.b64 b, {%2, %7};\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc_mxf4(256, 256, ID)), "r"(sa), "r"(sb), "r"(accumulate), "r"(kOperandHi)
+      : "memory");
+}
+// Whether the phase with this parity is complete; does not wait.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Arrives once on the barrier at this offset in both CTAs when every product issued so far is done.
+__device__ __forceinline__ void commit_both(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3))
       : "memory");
 }
 
@@ -366,10 +390,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 // ---------------------------------------------------------------------------
 // Large products: a pair of CTAs holds a 256 x 256 tile of C (128 rows each), so
 // that each SM reads half of B's tile from its shared memory and 8 KiB feed a
-// step of 128 cycles.  Two accumulators of 256 columns and two slots of scales
-// do not fit the 512 columns of tensor memory side by side: the accumulators
-// share 48 columns, which the epilogue reads first, and the next tile starts
-// once they are read.
+// step of 128 cycles.  Two accumulators of 256 columns and the slots of scales do
+// not fit the 512 columns of tensor memory side by side: the accumulators share
+// up to 128 columns, which the epilogue reads first, and the next tile starts once
+// they are read.
 // ---------------------------------------------------------------------------
 namespace pair {
 
@@ -380,16 +404,16 @@ constexpr uint32_t kABytes = BM * 128, kBBytes = BN / 2 * 128;
 constexpr uint32_t kScaleA = 2 * kScaleTile, kScaleB = 4 * kScaleTile;  // a stage: two tiles along k; B's 256 rows in both CTAs
 constexpr uint32_t kStageBytes = kABytes + kBBytes + kScaleA + kScaleB;
 constexpr uint32_t kSlotCols = 8 + 16;
-constexpr uint32_t kScaleCol = 512 - 2 * kSlotCols;
-constexpr uint32_t kAcc1 = kScaleCol - BN;  // 208: columns 208 .. 255 are shared
 constexpr int kChunk = 64;
-static_assert(BN - kAcc1 <= kChunk, "the shared columns lie in one chunk");
 
 template <typename T>
 struct Cfg {
   static constexpr int kStages = sizeof(T) == 4 ? 4 : 5;
+  static constexpr uint32_t kScaleCol = 512 - kStages * kSlotCols;  // a slot of scales for each stage
+  static constexpr uint32_t kAcc1 = kScaleCol - BN;                 // the second accumulator: columns kAcc1 .. 255 are shared
+  static_assert(BN - kAcc1 <= 2 * kChunk, "the shared columns lie in the two chunks read first");
   static constexpr uint32_t kRow = kChunk * sizeof(T) + 16;  // staging row, padded against bank conflicts
-  static constexpr int kBars = 2 * kStages + 6;              // full, empty; tfull x 2; early; scale slots x 2; drain
+  static constexpr int kBars = 2 * kStages + 4;              // full, empty; tfull x 2; early; drain
   static constexpr size_t kSmem = 1024 + kStages * kStageBytes + kEpiWarps * 32 * kRow + kBars * 8 + 16;
   static_assert(kSmem <= 232448, "shared memory");
 };
@@ -423,18 +447,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   auto empty_bar = [&](int s) { return bar0 + 8u * (S + s); };
   auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * S + a); };
   const uint32_t early_bar = bar0 + 8u * (2 * S + 2);
-  auto slot_bar = [&](int a) { return bar0 + 8u * (2 * S + 3 + a); };
-  const uint32_t drain_bar = bar0 + 8u * (2 * S + 5);
+  const uint32_t drain_bar = bar0 + 8u * (2 * S + 3);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
     }
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(tfull_bar(a), 1);
-      mbar_init(slot_bar(a), 1);
-    }
+    for (int a = 0; a < 2; ++a) mbar_init(tfull_bar(a), 1);
     mbar_init(early_bar, 2 * kEpiWarps);  // the leader's: the epilogue warps of both CTAs
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -505,60 +525,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      int stage = 0, slot = 0;
-      uint32_t phase = 0, slot_phase = 0;
-      bool ok = true;
+      // One thread issues everything: what it spends between two stages, the
+      // tensor cores wait for.
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true, ready = false;
+      // addresses of this stage: operand descriptor, scale descriptor, scales in tensor memory
+      const uint32_t a0 = kOperandLo | (smem0 >> 4), s0 = (smem0 + kABytes + kBBytes) >> 4, t0 = tmem + C::kScaleCol;
+      uint32_t a = a0, sa = s0, ta = t0;
       for (int t = first, k = 0; t < tiles && ok; t += npairs, ++k) {
         // the tile before last is read out and the shared columns of the last one too
         if (k > 0 && !mbar_wait(early_bar, static_cast<uint32_t>(k - 1) & 1u, ctl)) break;
         tc_fence_after();
-        const uint32_t d = tmem + (k & 1 ? kAcc1 : 0u);
-        for (int it = 0; it < kiters; ++it) {
-          // the slot's scales were last read by the products of two stages ago
-          if (!mbar_wait(full_bar(stage), phase, ctl) || !mbar_wait(slot_bar(slot), slot_phase ^ 1u, ctl)) {
+        const uint32_t d = tmem + (k & 1 ? C::kAcc1 : 0u);
+        uint32_t accumulate = 0;
+        int left = p.k;
+        for (int it = 0; it < kiters; ++it, left -= kStageK) {
+          // full again: the products that last read this stage's operands and scales are done
+          if (!ready && !mbar_wait(full_bar(stage), phase, ctl)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a = smem0 + stage * kStageBytes, b = a + kABytes, sa = b + kBBytes, sb = sa + kScaleA;
-          const uint32_t ta = tmem + kScaleCol + static_cast<uint32_t>(slot) * kSlotCols, tb = ta + 8;
-          const int steps = min(4, (p.k - it * kStageK + 63) / 64);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (2 * h >= steps) break;
-            scales_to_tmem_pair(ta + 4 * h, sa + h * kScaleTile);
-            scales_to_tmem_pair(tb + 8 * h, sb + h * kScaleTile);
-            scales_to_tmem_pair(tb + 8 * h + 4, sb + (2 + h) * kScaleTile);
+          const uint32_t b = a + (kABytes >> 4), sb = sa + (kScaleA >> 4), tb = ta + 8, empty = empty_bar(stage);
+          scales_to_tmem_pair(ta, sa);
+          scales_to_tmem_pair(tb, sb);
+          scales_to_tmem_pair(tb + 4, sb + 2 * (kScaleTile >> 4));
+          scales_to_tmem_pair(ta + 4, sa + (kScaleTile >> 4));
+          scales_to_tmem_pair(tb + 8, sb + (kScaleTile >> 4));
+          scales_to_tmem_pair(tb + 12, sb + 3 * (kScaleTile >> 4));
+          mma_mxf4_pair<0>(d, a, b, ta, tb, accumulate);
+          accumulate = 1;
+          // the next stage's addresses, and whether it is there, while the first product runs
+          const bool wrap = stage + 1 == S;
+          const uint32_t next_a = wrap ? a0 : a + (kStageBytes >> 4), next_sa = wrap ? s0 : sa + (kStageBytes >> 4),
+                         next_ta = wrap ? t0 : ta + kSlotCols;
+          stage = wrap ? 0 : stage + 1;
+          phase ^= wrap ? 1u : 0u;
+          ready = mbar_test(full_bar(stage), phase);
+          if (left > 192) {
+            mma_mxf4_pair<2>(d, a + 2, b + 2, ta, tb, 1);
+            mma_mxf4_pair<0>(d, a + 4, b + 4, ta + 4, tb + 8, 1);
+            mma_mxf4_pair<2>(d, a + 6, b + 6, ta + 4, tb + 8, 1);
+          } else {
+            if (left > 64) mma_mxf4_pair<2>(d, a + 2, b + 2, ta, tb, 1);
+            if (left > 128) mma_mxf4_pair<0>(d, a + 4, b + 4, ta + 4, tb + 8, 1);
           }
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            if (kk >= steps) break;
-            const uint32_t h = kk >> 1;
-            mma_mxf4_pair(d, sdesc_sw128(a + kk * 32, 16, 1024), sdesc_sw128(b + kk * 32, 16, 1024),
-                          idesc_mxf4(2 * BM, BN, 2 * (kk & 1)), ta + 4 * h, tb + 8 * h, (it | kk) != 0 ? 1u : 0u);
-          }
-          tc_commit_pair(empty_bar(stage));
-          tc_commit_pair(cluster_addr(empty_bar(stage), peer));
-          tc_commit_pair(slot_bar(slot));
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1u;
-          }
-          if (++slot == 2) {
-            slot = 0;
-            slot_phase ^= 1u;
-          }
+          commit_both(empty);
+          a = next_a;
+          sa = next_sa;
+          ta = next_ta;
         }
         if (!ok) break;
-        tc_commit_pair(tfull_bar(k & 1));
-        tc_commit_pair(cluster_addr(tfull_bar(k & 1), peer));
+        commit_both(tfull_bar(k & 1));
       }
       tc_commit_pair(drain_bar);
       mbar_wait_drain(drain_bar, 0, drain_ns > 1000000ull ? drain_ns : 1000000ull);
     }
     __syncwarp();
   } else {
-    // two warps a lane quarter, alternate chunks; the one with the shared columns first
+    // two warps a lane quarter, alternate chunks, those with the shared columns first
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     constexpr uint32_t kRow = C::kRow;
     uint8_t* stg = staging + (warp - 2) * 32 * kRow;
@@ -572,18 +598,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool ok = mbar_wait(tfull_bar(k & 1), (k >> 1) & 1, ctl);
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       tc_fence_after();
-      if (half == 1 && lane == 0) mbar_arrive_remote(early);  // this warp has left the tile before
       const long long row0 = static_cast<long long>(2 * tm + rank) * BM + quarter * 32;
 #pragma unroll 1
       for (int i = half; i < BN / kChunk; i += 2) {
         const int c0 = (k & 1 ? i : BN / kChunk - 1 - i) * kChunk;
         const long long col0 = static_cast<long long>(tn) * BN + c0;
         uint32_t r[2][32];
-        const uint32_t ta = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + (k & 1 ? kAcc1 : 0u) + static_cast<uint32_t>(c0);
+        const uint32_t ta = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + (k & 1 ? C::kAcc1 : 0u) + static_cast<uint32_t>(c0);
         tmem_ld_32x32(ta, r[0]);
         tmem_ld_32x32(ta + 32, r[1]);
         tmem_ld_wait();
-        if (i == 0) {
+        if (i == half) {  // this warp has left the tile before and the shared columns
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_remote(early);
