@@ -233,7 +233,7 @@ int quantize_impl(int count, const void* const* x, const int64_t* shapes, const 
     p.ntiles = static_cast<int>(tiles);
     if (p.ntiles == 0) continue;
     host::Timed timed(MUON_KERNEL_MX_QUANTIZE, s);
-    TRY_CUDA(mx::launch_quantize(p, dtype, sms, s));
+    TRY_CUDA(mx::launch_quantize(p, dtype, s));
   }
   return MUON_OK;
 }
@@ -281,7 +281,7 @@ int dequantize_impl(int count, const void* const* data, const void* const* scale
     p.ntiles = static_cast<int>(tiles);
     if (p.ntiles == 0) continue;
     host::Timed timed(MUON_KERNEL_MX_DEQUANTIZE, s);
-    TRY_CUDA(mx::launch_dequantize(p, dtype, sms, s));
+    TRY_CUDA(mx::launch_dequantize(p, dtype, s));
   }
   return MUON_OK;
 }

@@ -427,8 +427,8 @@ struct DequantParams {
   int nmat, ntiles;
 };
 
-cudaError_t launch_quantize(const QuantParams& p, int dtype, int sms, cudaStream_t s);
-cudaError_t launch_dequantize(const DequantParams& p, int dtype, int sms, cudaStream_t s);
+cudaError_t launch_quantize(const QuantParams& p, int dtype, cudaStream_t s);
+cudaError_t launch_dequantize(const DequantParams& p, int dtype, cudaStream_t s);
 
 // C = A B^T, A m x k and B n x k in 4 bits.
 struct ProductParams {
