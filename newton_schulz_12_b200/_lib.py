@@ -55,8 +55,8 @@ SIGNATURES = {
     "muon_layer_norm": (_I, [_L, _L, _P, _L, _I, _P, _P, _I, _F, _P, _L, _P, _P, _P]),
     "muon_layer_norm_backward": (_I, [_L, _L, _P, _L, _P, _L, _I, _P, _I, _P, _P, _P, _L, _P, _P, _P, _L, _P]),
     "muon_layer_norm_scratch_bytes": (_I, [_L, _L, ctypes.POINTER(ctypes.c_longlong)]),
-    "muon_mx_quantize": (_I, [_I, _PP, _I64P, _I64P, _I, _PP, _PP, _PP, _PP, _P]),
-    "muon_mx_dequantize": (_I, [_I, _PP, _PP, _I64P, _PP, _I, _P]),
+    "muon_mx_quantize": (_I, [_I, _P, _P, _P, _I, _P, _P, _P, _P, _P]),
+    "muon_mx_dequantize": (_I, [_I, _P, _P, _P, _P, _I, _P]),
     "muon_mx_product": (_I, [_L, _L, _L, _P, _P, _P, _P, _P, _L, _I, _P]),
     "muon_get_status": (_I, [_P]),
     "muon_last_error": (ctypes.c_char_p, []),

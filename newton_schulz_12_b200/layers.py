@@ -8,6 +8,8 @@ current stream, and allocate their results and scratch there.
 from __future__ import annotations
 
 import ctypes
+import functools
+from array import array
 
 import torch
 
@@ -22,12 +24,12 @@ _DTYPES = {torch.bfloat16: MUON_BF16, torch.float32: MUON_FP32, torch.float16: M
 
 def _on_stream(body, tensors, stream):
     """body(raw stream) on the device of ``tensors``, with ``stream`` current while it allocates."""
-    index = tensors[0].device.index
+    index = tensors[0].get_device()
     for t in tensors:
-        if t.device.index != index:
+        if t.get_device() != index:
             raise ValueError("all tensors must be on one device")
     if stream is None and index == torch.cuda.current_device():
-        return body(torch.cuda.current_stream(index).cuda_stream)
+        return body(torch.cuda.current_stream(index).cuda_stream if _raw_stream is None else _raw_stream(index))
     with torch.cuda.device(index):
         if stream is None:
             stream = torch.cuda.current_stream(index)
@@ -41,48 +43,58 @@ def _on_stream(body, tensors, stream):
             return body(stream.cuda_stream)
 
 
-def _matrix(t, name, dtype=None):
-    """Checks a 2-D CUDA matrix whose rows are contiguous; returns its row stride."""
+#: The current stream's handle without making a Stream object of it (1.2 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _tensor(t, name):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in _DTYPES:
-        raise ValueError(f"{name} must be bf16, fp16 or fp32, got {t.dtype}")
-    if dtype is not None and t.dtype != dtype:
+
+
+def _matrix(t, name, dtype=None):
+    """Checks a 2-D CUDA matrix whose rows are contiguous; returns its rows, columns and row stride."""
+    _tensor(t, name)
+    if dtype is None:
+        if t.dtype not in _DTYPES:
+            raise ValueError(f"{name} must be bf16, fp16 or fp32, got {t.dtype}")
+    elif t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
     rows, cols = t.shape
     ld, step = t.stride()
-    if cols > 1 and step != 1:
+    if step != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    if rows > 1 and ld < cols:
-        raise ValueError(f"{name} must not have overlapping rows")
-    return ld if rows > 1 else cols
+    if rows > 1:
+        if ld < cols:
+            raise ValueError(f"{name} must not have overlapping rows")
+        return rows, cols, ld
+    return rows, cols, cols
 
 
 def _rows_of(t, name, dtype=None, shape=None):
-    """A tensor (..., cols) as a matrix of rows, without copying."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() == 0:
-        raise ValueError(f"{name} must have at least one dimension")
+    """A tensor (..., cols) as a matrix of rows, without copying: its address, rows, columns and row stride."""
+    _tensor(t, name)
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
     if t.dim() != 2:
+        if t.dim() == 0:
+            raise ValueError(f"{name} must have at least one dimension")
         try:
             t = t.view(t.shape[:-1].numel(), t.shape[-1])
         except RuntimeError:
             raise ValueError(f"{name} of more than two dimensions must be viewable as rows of its last one") from None
-    return t, _matrix(t, name, dtype)
+    return (t.data_ptr(), *_matrix(t, name, dtype))
 
 
 def _vector(t, name, n, dtype):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in (torch.float32, dtype):
+    _tensor(t, name)
+    if t.dtype != dtype and t.dtype != torch.float32:
         raise ValueError(f"{name} must be fp32 or {dtype}, got {t.dtype}")
-    if t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous vector of {n} values")
+    return t.data_ptr()
 
 
 def _statistic(t, name, shape):
@@ -90,6 +102,12 @@ def _statistic(t, name, shape):
         raise ValueError(f"{name} must be an fp32 CUDA tensor")
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous, {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _like(x):
+    """A contiguous tensor of x's shape and type."""
+    return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
 
 
 def muon_layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, stream=None):
@@ -101,35 +119,49 @@ def muon_layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, stream=None):
     not overlap x); ``mean`` and ``rstd`` are fp32, one a row, as the backward
     pass takes them.
     """
-    m, ld = _rows_of(x, "x")
-    rows, cols = m.shape
+    xp, rows, cols, ld = _rows_of(x, "x")
     if cols == 0:
         raise ValueError("x must have at least one column")
     tensors = [x]
-    params = None
-    for t, name in ((weight, "weight"), (bias, "bias")):
-        if t is None:
-            continue
-        _vector(t, name, cols, x.dtype)
-        if params not in (None, t.dtype):
+    wp = bp = op = None
+    params = torch.float32
+    if weight is not None:
+        wp, params = _vector(weight, "weight", cols, x.dtype), weight.dtype
+        tensors.append(weight)
+    if bias is not None:
+        bp = _vector(bias, "bias", cols, x.dtype)
+        if weight is not None and bias.dtype != params:
             raise ValueError("weight and bias must have one type")
-        params = t.dtype
-        tensors.append(t)
+        params = bias.dtype
+        tensors.append(bias)
     if out is not None:
-        mo, ldo = _rows_of(out, "out", x.dtype, x.shape)
+        op, _, _, ldo = _rows_of(out, "out", x.dtype, x.shape)
         tensors.append(out)
 
     def body(s):
-        y, o, lo = (out, mo, ldo) if out is not None else (torch.empty(x.shape, dtype=x.dtype, device=x.device),) * 2 + (cols,)
-        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        y, yp, ldy = out, op, cols
+        if out is None:
+            y = _like(x)
+            yp = y.data_ptr()
+        else:
+            ldy = ldo
+        mean = torch.empty(rows, dtype=torch.float32, device=x.device)
+        if x.dim() != 2:
+            mean = mean.view(x.shape[:-1])
         rstd = torch.empty_like(mean)
-        check(_lib.lib().muon_layer_norm(
-            rows, cols, m.data_ptr(), ld, _DTYPES[x.dtype], None if weight is None else weight.data_ptr(),
-            None if bias is None else bias.data_ptr(), _DTYPES[params or torch.float32], eps, o.data_ptr(), lo,
-            mean.data_ptr(), rstd.data_ptr(), s))
+        check(_lib.lib().muon_layer_norm(rows, cols, xp, ld, _DTYPES[x.dtype], wp, bp, _DTYPES[params], eps, yp, ldy,
+                                         mean.data_ptr(), rstd.data_ptr(), s))
         return y, mean, rstd
 
     return _on_stream(body, tensors, stream)
+
+
+@functools.lru_cache(maxsize=1024)
+def _scratch_bytes(device, rows, cols):
+    """Bytes of scratch of a backward pass on the current device, ``device``."""
+    need = ctypes.c_longlong(0)
+    check(_lib.lib().muon_layer_norm_scratch_bytes(rows, cols, ctypes.byref(need)))
+    return need.value
 
 
 def muon_layer_norm_backward(dy, x, mean, rstd, weight=None, bias=False, params=True, out=None, stream=None):
@@ -141,38 +173,45 @@ def muon_layer_norm_backward(dy, x, mean, rstd, weight=None, bias=False, params=
     False); ``dbias`` the same type (fp32 where there is no weight), or None
     unless ``bias`` is true.
     """
-    m, ld = _rows_of(x, "x")
-    g, ldg = _rows_of(dy, "dy", x.dtype, x.shape)
-    rows, cols = m.shape
+    xp, rows, cols, ld = _rows_of(x, "x")
+    gp, _, _, ldg = _rows_of(dy, "dy", x.dtype, x.shape)
     if cols == 0:
         raise ValueError("x must have at least one column")
-    _statistic(mean, "mean", x.shape[:-1])
-    _statistic(rstd, "rstd", x.shape[:-1])
+    stats = x.shape[:-1]
+    mp, rp = _statistic(mean, "mean", stats), _statistic(rstd, "rstd", stats)
     tensors = [x, dy, mean, rstd]
+    wp = op = None
+    ptype = torch.float32
     if weight is not None:
-        _vector(weight, "weight", cols, x.dtype)
+        wp, ptype = _vector(weight, "weight", cols, x.dtype), weight.dtype
         tensors.append(weight)
-    ptype = torch.float32 if weight is None else weight.dtype
     want_w, want_b = weight is not None and params, bool(bias) and params
     if out is not None:
-        mo, ldo = _rows_of(out, "out", x.dtype, x.shape)
+        op, _, _, ldo = _rows_of(out, "out", x.dtype, x.shape)
         tensors.append(out)
 
     def body(s):
         lib = _lib.lib()
-        dx, o, lo = (out, mo, ldo) if out is not None else (torch.empty(x.shape, dtype=x.dtype, device=x.device),) * 2 + (cols,)
-        dw = torch.empty(cols, dtype=ptype, device=x.device) if want_w else None
-        db = torch.empty(cols, dtype=ptype, device=x.device) if want_b else None
-        need, scratch = ctypes.c_longlong(0), None
+        dx, dxp, lddx = out, op, cols
+        if out is None:
+            dx = _like(x)
+            dxp = dx.data_ptr()
+        else:
+            lddx = ldo
+        dw = db = scratch = dwp = dbp = sp = None
+        nbytes = 0
         if want_w or want_b:
-            check(lib.muon_layer_norm_scratch_bytes(rows, cols, ctypes.byref(need)))
-            if need.value:
-                scratch = torch.empty(need.value, dtype=torch.uint8, device=x.device)
-        check(lib.muon_layer_norm_backward(
-            rows, cols, g.data_ptr(), ldg, m.data_ptr(), ld, _DTYPES[x.dtype],
-            None if weight is None else weight.data_ptr(), _DTYPES[ptype], mean.data_ptr(), rstd.data_ptr(), o.data_ptr(), lo,
-            None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr(),
-            None if scratch is None else scratch.data_ptr(), need.value, s))
+            nbytes = _scratch_bytes(x.get_device(), rows, cols)
+            scratch = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+            sp = scratch.data_ptr() if nbytes else None
+        if want_w:
+            dw = torch.empty_like(weight)
+            dwp = dw.data_ptr()
+        if want_b:
+            db = torch.empty(cols, dtype=ptype, device=x.device) if weight is None else torch.empty_like(weight)
+            dbp = db.data_ptr()
+        check(lib.muon_layer_norm_backward(rows, cols, gp, ldg, xp, ld, _DTYPES[x.dtype], wp, _DTYPES[ptype], mp, rp, dxp,
+                                           lddx, dwp, dbp, sp, nbytes, s))
         return dx, dw, db
 
     return _on_stream(body, tensors, stream)
@@ -197,7 +236,7 @@ class MxMatrix:
                 raise ValueError(f"{name} must be a uint8 tensor")
             if t.shape != shape or not t.is_contiguous():
                 raise ValueError(f"{name} of a {rows} x {cols} matrix must be contiguous, {shape}, got {tuple(t.shape)}")
-        if scales.device != data.device:
+        if scales.get_device() != data.get_device():
             raise ValueError("data and scales must be on one device")
         self.rows, self.cols, self._buffer, self._data, self._scales, self._at = rows, cols, None, data, scales, None
 
@@ -255,7 +294,7 @@ class MxMatrix:
     def _pointers(self):
         if self._buffer is not None:
             p = self._buffer.data_ptr() + self._at
-            return p, p + self._bytes(self.rows, self.cols)[0]
+            return p, p + self.rows * ((self.cols + 31) >> 5) * 16
         return self._data.data_ptr(), self._scales.data_ptr()
 
     def __repr__(self):
@@ -265,12 +304,8 @@ class MxMatrix:
 def _mx(q, name):
     if not isinstance(q, MxMatrix):
         raise ValueError(f"{name} must be an MxMatrix")
-    if q.device.type != "cuda":
+    if not (q._data if q._buffer is None else q._buffer).is_cuda:
         raise ValueError(f"{name} must be a CUDA matrix")
-
-
-def _array(kind, values):
-    return (kind * max(1, len(values)))(*values)
 
 
 def muon_mx_quantize(x, rows=True, cols=False, out=None, stream=None):
@@ -290,15 +325,16 @@ def muon_mx_quantize(x, rows=True, cols=False, out=None, stream=None):
     if not xs:
         return []
     dtype = xs[0].dtype if isinstance(xs[0], torch.Tensor) else None
-    strides = [_matrix(t, f"x[{i}]", dtype) for i, t in enumerate(xs)]
-    shapes = [tuple(t.shape) for t in xs]
+    if dtype not in _DTYPES:
+        raise ValueError(f"x must be bf16, fp16 or fp32 CUDA matrices, got {dtype}")
+    sizes = [_matrix(t, "x", dtype) for t in xs]
     given, tensors = None, list(xs)
     if out is not None:
         given = [out] if single else list(out)
         if len(given) != len(xs):
             raise ValueError("one out for each matrix is required")
         given = [tuple(g) if rows and cols else (g,) for g in given]
-        for i, (g, (r, c)) in enumerate(zip(given, shapes)):
+        for i, (g, (r, c, _)) in enumerate(zip(given, sizes)):
             want = ([(r, c)] if rows else []) + ([(c, r)] if cols else [])
             for q, w in zip(g, want):
                 _mx(q, f"out[{i}]")
@@ -311,56 +347,80 @@ def muon_mx_quantize(x, rows=True, cols=False, out=None, stream=None):
     def body(s):
         forms = given
         if forms is None:
-            at, places = 0, []
-            for r, c in shapes:
-                for a, b in ([(r, c)] if rows else []) + ([(c, r)] if cols else []):
-                    places.append((at, a, b))
-                    at += sum(MxMatrix._bytes(a, b))
+            # every form's data and scales in one buffer, each at a multiple of 16 bytes
+            at, made, row, col = 0, [], [], []
+            for r, c, _ in sizes:
+                tiles = ((r + 127) >> 7) * ((c + 127) >> 7) * 512
+                if rows:
+                    data = r * ((c + 31) >> 5) * 16
+                    made.append((at, r, c))
+                    row.append((at, at + data))
+                    at += data + tiles
+                if cols:
+                    data = c * ((r + 31) >> 5) * 16
+                    made.append((at, c, r))
+                    col.append((at, at + data))
+                    at += data + tiles
             buffer = torch.empty(at, dtype=torch.uint8, device=xs[0].device)
-            made = [MxMatrix._within(buffer, *place) for place in places]
-            forms = list(zip(made[0::2], made[1::2])) if rows and cols else [(q,) for q in made]
-        row = [f[0]._pointers() for f in forms] if rows else None
-        col = [f[-1]._pointers() for f in forms] if cols else None
-        V, L = ctypes.c_void_p, ctypes.c_int64
-
-        def column(pairs, k):
-            return None if pairs is None else _array(V, [p[k] for p in pairs])
-
-        check(_lib.lib().muon_mx_quantize(
-            len(xs), _array(V, [t.data_ptr() for t in xs]), _array(L, [v for sh in shapes for v in sh]), _array(L, strides),
-            _DTYPES[dtype], column(row, 0), column(row, 1), column(col, 0), column(col, 1), s))
+            base = buffer.data_ptr()
+            made = [MxMatrix._within(buffer, *place) for place in made]
+            forms = list(zip(made[0::2], made[1::2])) if rows and cols else made
+        else:
+            base = 0
+            row = [f[0]._pointers() for f in given] if rows else []
+            col = [f[-1]._pointers() for f in given] if cols else []
+        values = array("q", [t.data_ptr() for t in xs])
+        values.extend([v for r, c, _ in sizes for v in (r, c)])
+        values.extend([ld for _, _, ld in sizes])
+        for pairs in (row, col):
+            values.extend([base + d for d, _ in pairs])
+            values.extend([base + q for _, q in pairs])
+        n, p = 8 * len(xs), values.buffer_info()[0]
+        rd, cd = (p + 4 * n if rows else None), (p + (6 * n if rows else 4 * n) if cols else None)
+        check(_lib.lib().muon_mx_quantize(len(xs), p, p + n, p + 3 * n, _DTYPES[dtype], rd, rd and rd + n, cd, cd and cd + n, s))
         if out is not None:
             return out
-        got = forms if rows and cols else [f[0] for f in forms]
-        return got[0] if single else got
+        return forms[0] if single else forms
 
     return _on_stream(body, tensors, stream)
 
 
 def muon_mx_dequantize(q, dtype=torch.bfloat16, stream=None):
     """The values of an ``MxMatrix``, or of each of a list in one launch, as contiguous
-    matrices of ``dtype``: exact in bf16 and fp32, rounded in fp16."""
+    matrices of ``dtype``: exact in bf16 and fp32, rounded in fp16.
+
+    The matrices of a list are views of one allocation.
+    """
     single = isinstance(q, MxMatrix)
     qs = [q] if single else list(q)
     if dtype not in _DTYPES:
         raise ValueError(f"dtype must be bf16, fp16 or fp32, got {dtype}")
     if not qs:
         return []
-    tensors = []
-    for i, m in enumerate(qs):
-        _mx(m, f"q[{i}]")
-        tensors += m._tensors()
+    tensors = {}
+    for m in qs:
+        _mx(m, "q")
+        for t in m._tensors():
+            tensors[id(t)] = t
 
     def body(s):
-        ys = [torch.empty(m.shape, dtype=dtype, device=m.device) for m in qs]
+        if single:
+            ys = [torch.empty(q.rows, q.cols, dtype=dtype, device=q.device)]
+        else:  # one allocation, each matrix on a 16-byte boundary
+            step = 16 // dtype.itemsize
+            spans = [-(-m.rows * m.cols // step) * step for m in qs]
+            parts = torch.empty(sum(spans), dtype=dtype, device=qs[0].device).split(spans)
+            ys = [(t if n == m.rows * m.cols else t[: m.rows * m.cols]).view(m.rows, m.cols) for t, n, m in zip(parts, spans, qs)]
         places = [m._pointers() for m in qs]
-        V = ctypes.c_void_p
-        check(_lib.lib().muon_mx_dequantize(
-            len(qs), _array(V, [p[0] for p in places]), _array(V, [p[1] for p in places]),
-            _array(ctypes.c_int64, [v for m in qs for v in m.shape]), _array(V, [y.data_ptr() for y in ys]), _DTYPES[dtype], s))
+        values = array("q", [d for d, _ in places])
+        values.extend([q for _, q in places])
+        values.extend([v for m in qs for v in (m.rows, m.cols)])
+        values.extend([y.data_ptr() for y in ys])
+        n, p = 8 * len(qs), values.buffer_info()[0]
+        check(_lib.lib().muon_mx_dequantize(len(qs), p, p + n, p + 2 * n, p + 4 * n, _DTYPES[dtype], s))
         return ys[0] if single else ys
 
-    return _on_stream(body, tensors, stream)
+    return _on_stream(body, list(tensors.values()), stream)
 
 
 def muon_mx_product(a, b, dtype=torch.bfloat16, out=None, stream=None):
@@ -371,13 +431,12 @@ def muon_mx_product(a, b, dtype=torch.bfloat16, out=None, stream=None):
     """
     _mx(a, "a")
     _mx(b, "b")
-    m, k = a.shape
-    n = b.rows
+    m, k, n = a.rows, a.cols, b.rows
     if b.cols != k:
         raise ValueError(f"a and b must have equal columns, got {k} and {b.cols}")
     tensors = a._tensors() + b._tensors()
     if out is not None:
-        ldo = _matrix(out, "out")
+        _, _, ldo = _matrix(out, "out")
         if out.shape != (m, n):
             raise ValueError(f"out must be {(m, n)}, got {tuple(out.shape)}")
         dtype = out.dtype
@@ -386,7 +445,7 @@ def muon_mx_product(a, b, dtype=torch.bfloat16, out=None, stream=None):
         raise ValueError(f"dtype must be bf16, fp16 or fp32, got {dtype}")
 
     def body(s):
-        y, ld = (out, ldo) if out is not None else (torch.empty(m, n, dtype=dtype, device=a.device), n)
+        y, ld = (out, ldo) if out is not None else (torch.empty((m, n), dtype=dtype, device=a.device), n)
         check(_lib.lib().muon_mx_product(m, n, k, *a._pointers(), *b._pointers(), y.data_ptr(), ld, _DTYPES[dtype], s))
         return y
 
