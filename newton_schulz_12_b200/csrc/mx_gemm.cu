@@ -92,9 +92,9 @@ __device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uin
 }
 
 // Pair forms: the box lands in this CTA's shared memory and is credited to the
-// barrier `cbar` of the pair's leader; a copy of scales runs in both CTAs, each
-// from its own shared memory; a product takes 128 rows of A and half of B's rows
-// from each CTA.
+// barrier `cbar` of the pair's leader; a product takes 128 rows of A and half of
+// B's rows from each CTA, and all scales that its rows need from its own tensor
+// memory.
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* map, uint32_t cbar, int c0, int c1) {
   asm volatile(
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
@@ -105,13 +105,21 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* map, 
 // Descriptors as two words: only the low one (the address) changes in the issue loop.
 constexpr uint32_t kOperandHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // 8-row groups 1 KiB apart, 128-byte swizzle
 constexpr uint32_t kOperandLo = 1u << 16;
-constexpr uint32_t kScaleHi = (128u >> 4) | (1u << 14);                  // 8-row groups of 16-byte rows, no swizzle
-__device__ __forceinline__ void scales_to_tmem_pair(uint32_t taddr, uint32_t lo) {
+// A warp's lane quarter of tensor memory, 8 or 16 columns from `taddr`, one word a lane and column.
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
-      "{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
-      "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr), "r"(lo), "r"(kScaleHi)
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 template <int ID>
 __device__ __forceinline__ void mma_mxf4_pair(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t sa, uint32_t sb, uint32_t accumulate) {
   asm volatile(
@@ -165,11 +173,26 @@ __device__ __forceinline__ void store_chunk(T* out, const ProductParams& p, cons
         *reinterpret_cast<uint4*>(out + (row0 + r) * p.ldo + col0 + u * kVec) =
             *reinterpret_cast<const uint4*>(stg + r * stg_row + u * 16);
     }
-  } else {
-    for (int e = lane; e < 32 * CW; e += 32) {
-      const int r = e / CW, c = e % CW;
-      if (row0 + r < p.m && col0 + c < p.n)
-        out[(row0 + r) * p.ldo + col0 + c] = reinterpret_cast<const T*>(stg + r * stg_row)[c];
+  } else {  // value by value, eight under way at a time
+    const int rows = p.m - row0 < 32 ? static_cast<int>(p.m - row0) : 32;
+    constexpr int kPer = CW / 32, kBatch = 8 / kPer;
+    bool in[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) in[k] = col0 + lane + 32 * k < p.n;
+    T* dst = out + row0 * p.ldo + col0 + lane;
+    for (int r0 = 0; r0 < rows; r0 += kBatch) {
+      T v[kBatch][kPer];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) v[i][k] = reinterpret_cast<const T*>(stg + (r0 + i) * stg_row)[lane + 32 * k];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+          if (r0 + i < rows && in[k]) dst[32 * k] = v[i][k];
+        dst += p.ldo;
+      }
     }
   }
 }
@@ -394,12 +417,16 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 // not fit the 512 columns of tensor memory side by side: the accumulators share
 // up to 128 columns, which the epilogue reads first, and the next tile starts once
 // they are read.
+//
+// Four warps carry each stage's scales from shared to tensor memory.  tcgen05.cp
+// does it, too, but takes its turn with the products: six copies a stage made
+// 8192^3 take 244 us instead of 208.
 // ---------------------------------------------------------------------------
 namespace pair {
 
 constexpr int BN = 256;
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kThreads = 64 + 32 * kEpiWarps + 128;  // copier, issuer, epilogue, scales
 constexpr uint32_t kABytes = BM * 128, kBBytes = BN / 2 * 128;
 constexpr uint32_t kScaleA = 2 * kScaleTile, kScaleB = 4 * kScaleTile;  // a stage: two tiles along k; B's 256 rows in both CTAs
 constexpr uint32_t kStageBytes = kABytes + kBBytes + kScaleA + kScaleB;
@@ -413,7 +440,7 @@ struct Cfg {
   static constexpr uint32_t kAcc1 = kScaleCol - BN;                 // the second accumulator: columns kAcc1 .. 255 are shared
   static_assert(BN - kAcc1 <= 2 * kChunk, "the shared columns lie in the two chunks read first");
   static constexpr uint32_t kRow = kChunk * sizeof(T) + 16;  // staging row, padded against bank conflicts
-  static constexpr int kBars = 2 * kStages + 4;              // full, empty; tfull x 2; early; drain
+  static constexpr int kBars = 4 * kStages + 4;              // full, empty, scales landed, scales ready; tfull x 2; early; drain
   static constexpr size_t kSmem = 1024 + kStages * kStageBytes + kEpiWarps * 32 * kRow + kBars * 8 + 16;
   static_assert(kSmem <= 232448, "shared memory");
 };
@@ -448,11 +475,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * S + a); };
   const uint32_t early_bar = bar0 + 8u * (2 * S + 2);
   const uint32_t drain_bar = bar0 + 8u * (2 * S + 3);
+  auto landed_bar = [&](int s) { return bar0 + 8u * (2 * S + 4 + s); };
+  auto ready_bar = [&](int s) { return bar0 + 8u * (3 * S + 4 + s); };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
+      mbar_init(landed_bar(s), 1);
+      mbar_init(ready_bar(s), 8);  // the leader's: the scale warps of both CTAs
     }
     for (int a = 0; a < 2; ++a) mbar_init(tfull_bar(a), 1);
     mbar_init(early_bar, 2 * kEpiWarps);  // the leader's: the epilogue warps of both CTAs
@@ -502,16 +533,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             break;
           }
           const uint32_t fbar = cluster_addr(full_bar(stage), 0);
-          if (rank == 0) {
-            mbar_arrive_expect_tx(full_bar(stage), 2 * kStageBytes);  // what lies beyond a matrix comes as zeros and counts
-            issued |= 1u << stage;
-            parity = (parity & ~(1u << stage)) | (phase << stage);
-          }
+          // what lies beyond a matrix comes as zeros and counts
+          if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2 * (kABytes + kBBytes));
+          mbar_arrive_expect_tx(landed_bar(stage), kScaleA + kScaleB);
+          issued |= 1u << stage;
+          parity = (parity & ~(1u << stage)) | (phase << stage);
           const uint32_t a = smem0 + stage * kStageBytes, b = a + kABytes, sa = b + kBBytes, sb = sa + kScaleA;
+          tma_load_2d(sa, &p.sa, landed_bar(stage), it * 256, 2 * tm + rank);
+          tma_load_2d(sb, &p.sb, landed_bar(stage), it * 256, 2 * tn);
           tma_load_2d_pair(a, &p.a, fbar, it * 128, (2 * tm + rank) * BM);
           tma_load_2d_pair(b, &p.b, fbar, it * 128, tn * BN + rank * (BN / 2));
-          tma_load_2d_pair(sa, &p.sa, fbar, it * 256, 2 * tm + rank);
-          tma_load_2d_pair(sb, &p.sb, fbar, it * 256, 2 * tn);
           if (++stage == S) {
             stage = 0;
             phase ^= 1u;
@@ -520,7 +551,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (!ok)
         for (int s = 0; s < S; ++s)
-          if (issued & (1u << s)) mbar_wait_drain(full_bar(s), (parity >> s) & 1u, drain_ns);
+          if (issued & (1u << s)) {
+            if (rank == 0) mbar_wait_drain(full_bar(s), (parity >> s) & 1u, drain_ns);
+            mbar_wait_drain(landed_bar(s), (parity >> s) & 1u, drain_ns);
+          }
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -530,9 +564,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true, ready = false;
-      // addresses of this stage: operand descriptor, scale descriptor, scales in tensor memory
-      const uint32_t a0 = kOperandLo | (smem0 >> 4), s0 = (smem0 + kABytes + kBBytes) >> 4, t0 = tmem + C::kScaleCol;
-      uint32_t a = a0, sa = s0, ta = t0;
+      // this stage's operand descriptor and scales in tensor memory
+      const uint32_t a0 = kOperandLo | (smem0 >> 4), t0 = tmem + C::kScaleCol;
+      uint32_t a = a0, ta = t0;
       for (int t = first, k = 0; t < tiles && ok; t += npairs, ++k) {
         // the tile before last is read out and the shared columns of the last one too
         if (k > 0 && !mbar_wait(early_bar, static_cast<uint32_t>(k - 1) & 1u, ctl)) break;
@@ -542,27 +576,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int left = p.k;
         for (int it = 0; it < kiters; ++it, left -= kStageK) {
           // full again: the products that last read this stage's operands and scales are done
-          if (!ready && !mbar_wait(full_bar(stage), phase, ctl)) {
+          if (!ready && (!mbar_wait(full_bar(stage), phase, ctl) || !mbar_wait(ready_bar(stage), phase, ctl))) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t b = a + (kABytes >> 4), sb = sa + (kScaleA >> 4), tb = ta + 8, empty = empty_bar(stage);
-          scales_to_tmem_pair(ta, sa);
-          scales_to_tmem_pair(tb, sb);
-          scales_to_tmem_pair(tb + 4, sb + 2 * (kScaleTile >> 4));
-          scales_to_tmem_pair(ta + 4, sa + (kScaleTile >> 4));
-          scales_to_tmem_pair(tb + 8, sb + (kScaleTile >> 4));
-          scales_to_tmem_pair(tb + 12, sb + 3 * (kScaleTile >> 4));
+          const uint32_t b = a + (kABytes >> 4), tb = ta + 8, empty = empty_bar(stage);
           mma_mxf4_pair<0>(d, a, b, ta, tb, accumulate);
           accumulate = 1;
           // the next stage's addresses, and whether it is there, while the first product runs
           const bool wrap = stage + 1 == S;
-          const uint32_t next_a = wrap ? a0 : a + (kStageBytes >> 4), next_sa = wrap ? s0 : sa + (kStageBytes >> 4),
-                         next_ta = wrap ? t0 : ta + kSlotCols;
+          const uint32_t next_a = wrap ? a0 : a + (kStageBytes >> 4), next_ta = wrap ? t0 : ta + kSlotCols;
           stage = wrap ? 0 : stage + 1;
           phase ^= wrap ? 1u : 0u;
-          ready = mbar_test(full_bar(stage), phase);
+          ready = mbar_test(full_bar(stage), phase) && mbar_test(ready_bar(stage), phase);
           if (left > 192) {
             mma_mxf4_pair<2>(d, a + 2, b + 2, ta, tb, 1);
             mma_mxf4_pair<0>(d, a + 4, b + 4, ta + 4, tb + 8, 1);
@@ -573,7 +600,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           commit_both(empty);
           a = next_a;
-          sa = next_sa;
           ta = next_ta;
         }
         if (!ok) break;
@@ -583,6 +609,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_wait_drain(drain_bar, 0, drain_ns > 1000000ull ? drain_ns : 1000000ull);
     }
     __syncwarp();
+  } else if (warp >= 2 + kEpiWarps) {
+    // scales of each stage, in both CTAs: a warp a lane quarter, all with the same words
+    const uint32_t mine = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int t = first; t < tiles && ok; t += npairs) {
+      for (int it = 0; it < kiters; ++it) {
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(landed_bar(stage), phase, ctl));
+        if (!ok) break;
+        tc_fence_after();  // the products that last read this slot are done: the stage was empty
+        const uint8_t* sa = smem + stage * kStageBytes + kABytes + kBBytes + 16 * lane;
+        const uint8_t* sb = sa + kScaleA;
+        uint32_t r[24];
+        auto take = [&](int at, const uint8_t* src) { *reinterpret_cast<uint4*>(r + at) = *reinterpret_cast<const uint4*>(src); };
+        take(0, sa);
+        take(4, sa + kScaleTile);
+        take(8, sb);  // B: 128 rows, the next 128; then the same of the second tile along k
+        take(12, sb + 2 * kScaleTile);
+        take(16, sb + kScaleTile);
+        take(20, sb + 3 * kScaleTile);
+        const uint32_t ta = tmem + mine + C::kScaleCol + static_cast<uint32_t>(stage) * kSlotCols;
+        tmem_st_x8(ta, r);
+        tmem_st_x16(ta + 8, r + 8);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(cluster_addr(ready_bar(stage), 0));
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
   } else {
     // two warps a lane quarter, alternate chunks, those with the shared columns first
     const int quarter = warp & 3, half = (warp - 2) >> 2;
