@@ -115,39 +115,6 @@ __global__ void __launch_bounds__(kLoopThreads) backward_loop_kernel(const BwdPa
   }
 }
 
-// Partial column sums of dy xhat and dy: block (i, j) takes 32 columns and the
-// j-th of `parts` runs of rows, and writes partial j.
-template <typename T>
-__global__ void __launch_bounds__(256) column_kernel(const BwdParams p) {
-  __shared__ float sw[8][33], sb[8][33];
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + tx;
-  const long long per = (p.rows + p.parts - 1) / p.parts;
-  const long long r0 = per * blockIdx.y;
-  const long long r1 = r0 + per < p.rows ? r0 + per : p.rows;
-  float w = 0.f, b = 0.f;
-  if (c < p.cols) {
-    for (long long r = r0 + ty; r < r1; r += 8) {
-      const float d = to_f(static_cast<const T*>(p.dy)[r * p.lddy + c]);
-      const float xhat = (to_f(static_cast<const T*>(p.x)[r * p.ldx + c]) - p.mean[r]) * p.rstd[r];
-      w = fmaf(d, xhat, w);
-      b += d;
-    }
-  }
-  sw[ty][tx] = w;
-  sb[ty][tx] = b;
-  __syncthreads();
-  if (ty == 0 && c < p.cols) {
-    for (int k = 1; k < 8; ++k) {
-      w += sw[k][tx];
-      b += sb[k][tx];
-    }
-    float* out = p.partials + static_cast<long long>(blockIdx.y) * 2 * p.cols;
-    out[c] = w;
-    out[p.cols + c] = b;
-  }
-}
-
 // dw and db from the partials, summed in a fixed order; 32 columns a block.
 template <typename P>
 __global__ void __launch_bounds__(1024) finish_kernel(const BwdParams p) {
@@ -213,6 +180,53 @@ template <typename T, int VEC>
 struct __align__(16) Pack {
   T v[VEC];
 };
+
+// Partial column sums of dy xhat and dy, where rows are too wide to add them up
+// on the way: block (i, j) takes 32 V columns, V a thread in one access, and the
+// j-th of `parts` runs of rows, and writes partial j.
+template <typename T, int V>
+__global__ void __launch_bounds__(256) column_kernel(const BwdParams p) {
+  __shared__ float part[8][32 * V + 1];
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int c = (blockIdx.x * 32 + tx) * V;
+  const long long per = (p.rows + p.parts - 1) / p.parts;
+  const long long r0 = per * blockIdx.y;
+  const long long r1 = r0 + per < p.rows ? r0 + per : p.rows;
+  float w[V], b[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) w[k] = b[k] = 0.f;
+  if (c < p.cols) {
+    const T* x = static_cast<const T*>(p.x) + c;
+    const T* dy = static_cast<const T*>(p.dy) + c;
+#pragma unroll 4
+    for (long long r = r0 + ty; r < r1; r += 8) {
+      const Pack<T, V> xv = *reinterpret_cast<const Pack<T, V>*>(x + r * p.ldx);
+      const Pack<T, V> dv = *reinterpret_cast<const Pack<T, V>*>(dy + r * p.lddy);
+      const float mean = p.mean[r], rstd = p.rstd[r];
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const float d = to_f(dv.v[k]);
+        w[k] = fmaf(d, (to_f(xv.v[k]) - mean) * rstd, w[k]);
+        b[k] += d;
+      }
+    }
+  }
+  float* out = p.partials + static_cast<long long>(blockIdx.y) * 2 * p.cols;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (h) __syncthreads();
+#pragma unroll
+    for (int k = 0; k < V; ++k) part[ty][tx * V + k] = h ? b[k] : w[k];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 32 * V; i += 256) {
+      const int col = blockIdx.x * 32 * V + i;
+      if (col >= p.cols) break;
+      float v = part[0][i];
+      for (int k = 1; k < 8; ++k) v += part[k][i];
+      out[h * p.cols + col] = v;
+    }
+  }
+}
 
 // Two fp32 values in one register pair: the packed operations of common.cuh
 // work on both at once, each rounded as alone.
@@ -879,7 +893,12 @@ cudaError_t backward(BwdParams p, int sms, cudaStream_t s) {
     }
   }
   if (e != cudaSuccess || !(p.dweight || p.dbias)) return e;
-  if (!held && p.parts > 0) column_kernel<T><<<dim3((p.cols + 31) / 32, p.parts), 256, 0, s>>>(p);
+  if (!held && p.parts > 0) {
+    if (vec)
+      column_kernel<T, V><<<dim3((p.cols + 32 * V - 1) / (32 * V), p.parts), 256, 0, s>>>(p);
+    else
+      column_kernel<T, 1><<<dim3((p.cols + 31) / 32, p.parts), 256, 0, s>>>(p);
+  }
   finish_kernel<P><<<(p.cols + 31) / 32, 1024, 0, s>>>(p);
   return cudaGetLastError();
 }
