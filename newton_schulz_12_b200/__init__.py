@@ -16,7 +16,7 @@ import ctypes
 
 import torch
 
-from . import _lib
+from . import _lib, layers
 from ._lib import (MUON_BF16, MUON_CAUTIOUS_WD, MUON_FP16, MUON_FP32, MuonError, check, ptr_array,
                    shape_array)
 from .layers import (MxMatrix, muon_layer_norm, muon_layer_norm_backward, muon_mx_dequantize,
@@ -245,11 +245,15 @@ class MuonStepPlan(_Replayable):
     alive and keep their storage while the plan is used.  ``capture`` records a
     step in a CUDA graph and ``replay`` runs it (one step per replay).  With
     any of ``cautious_wd``, ``neuron_state`` or ``schedule`` the calls go to
-    muon_step_ex (options as there; a schedule fixes the step count).
+    muon_step_ex (options as there; a schedule fixes the step count).  With
+    ``mx_forms`` every call ends by writing the new weights' 4-bit forms, for
+    the layer's forward and backward products: ``plan.mx_forms[i]`` is the pair
+    (rows, columns) of ``params[i]``, filled at construction, too.
     """
 
     def __init__(self, params, grads, momentum_bufs, beta=0.95, nesterov=True, lr=0.05, wd=0.0,
-                 steps=5, cautious_wd=False, neuron_state=None, beta2=0.95, schedule=None):
+                 steps=5, cautious_wd=False, neuron_state=None, beta2=0.95, schedule=None,
+                 mx_forms=False):
         self.params, self.grads, self.bufs = list(params), list(grads), list(momentum_bufs)
         if not (len(self.params) == len(self.grads) == len(self.bufs)):
             raise ValueError("params, grads and momentum_bufs must have the same length")
@@ -290,6 +294,12 @@ class MuonStepPlan(_Replayable):
         self._fn_ex = None
         if self._table is not None or self._state is not None or cautious_wd:
             self._fn_ex = _lib.lib().muon_step_ex
+        self.mx_forms, self._quantize = None, None
+        if mx_forms:
+            self.mx_forms = muon_mx_quantize(self.params, rows=True, cols=True)
+            pairs = [(r._pointers(), c._pointers()) for r, c in self.mx_forms]
+            self._quantize = layers._marshal_quantize(self.params, [(*s, s[1]) for s in shapes],
+                                                      [r for r, _ in pairs], [c for _, c in pairs])
 
     def update(self, beta=None, nesterov=None, lr=None, wd=None, steps=None):
         """Change hyper-parameters for the following calls (None keeps a value)."""
@@ -307,9 +317,12 @@ class MuonStepPlan(_Replayable):
             flags, beta2 = self._ex
             check(self._fn_ex(len(self.params), self._p, self._g, self._m, self._s, beta, nest, lr,
                               wd, steps, self._table, flags, self._state, beta2, _stream(stream)))
-            return
-        check(self._fn(len(self.params), self._p, self._g, self._m, self._s, beta, nest, lr, wd,
-                       steps, _stream(stream)))
+        else:
+            check(self._fn(len(self.params), self._p, self._g, self._m, self._s, beta, nest, lr, wd,
+                           steps, _stream(stream)))
+        if self._quantize is not None:
+            self._quantize(_stream(stream))
+
 
 class MuonNsPlan(_Replayable):
     """muon_ns_orthogonalize with its arguments marshalled once, for a fixed

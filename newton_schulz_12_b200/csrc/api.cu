@@ -1326,6 +1326,13 @@ int workspace_status(cudaStream_t s, int** status) {
 
 unsigned long long wait_timeout_ns() { return g_timeout_ns; }
 
+int take_injection() {
+  std::lock_guard<std::mutex> lk(g_mu);
+  const int mode = g_inject;
+  g_inject = 0;
+  return mode;
+}
+
 int encode_2d(CUtensorMap* map, const void* base, bool words, uint64_t inner, uint64_t rows, uint64_t stride_bytes,
               uint32_t box_inner, uint32_t box_rows) {
   MUON_TRY(get_encoder());

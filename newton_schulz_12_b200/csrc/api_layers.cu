@@ -315,6 +315,7 @@ int product_impl(long long m, long long n, long long k, const void* a_data, cons
   mx::ProductParams p{};
   TRY(host::workspace_status(s, &p.status));
   p.timeout_ns = host::wait_timeout_ns();
+  p.inject = host::take_injection();
   // few rows of A: B's rows take the tensor cores' 128-row side
   p.transposed = m <= 64 && n > m;
   p.m = static_cast<int>(p.transposed ? n : m);
@@ -325,7 +326,7 @@ int product_impl(long long m, long long n, long long k, const void* a_data, cons
   p.a_scales = p.transposed ? b_scales : a_scales;
   p.b_scales = p.transposed ? a_scales : b_scales;
   const uint64_t row = static_cast<uint64_t>(mx::data_stride(k));
-  const int tile_n = mx::product_tile_n(p.m, p.n, sms);
+  const int tile_n = mx::product_tile_n(p.m, p.n, p.k, sms);
   TRY(host::encode_2d(&p.a, p.transposed ? b_data : a_data, false, row, p.m, row, 128, 128));
   TRY(host::encode_2d(&p.b, p.transposed ? a_data : b_data, false, row, p.n, row, 128, tile_n == 256 ? 128 : tile_n));
   if (tile_n == 256) {

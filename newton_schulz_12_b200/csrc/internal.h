@@ -442,11 +442,12 @@ struct ProductParams {
   int transposed;        // 1: a, m are the caller's B and n: out[col * ldo + row]
   int* status;
   unsigned long long timeout_ns;
+  int inject;            // 1: withhold one operand copy in block 0 (timeout-path test)
 };
 
-// Columns of the tiles of an m x n product, m >= n where n <= 64: b's box has as
-// many rows, or half as many for tiles of 256 (a pair of CTAs).
-int product_tile_n(int m, int n, int sms);
+// Columns of the tiles of an m x n product over k, m >= n where n <= 64: b's box
+// has as many rows, or half as many for tiles of 256 (a pair of CTAs).
+int product_tile_n(int m, int n, int k, int sms);
 cudaError_t launch_product(const ProductParams& p, int dtype, int sms, cudaStream_t s);
 // Reads and clears the current device's status word of captured launches.
 cudaError_t take_captured_status(int* value);
@@ -461,6 +462,7 @@ void clear_error();
 int device_sms(int* sms);                       // checks the device, too
 int workspace_status(cudaStream_t s, int** status);  // device status word of (current device, stream)
 unsigned long long wait_timeout_ns();
+int take_injection();                           // the pending fault-injection mode, which it clears
 // A 2-D map of bytes with 128-byte swizzle (`words` false) or of 4-byte words without.
 int encode_2d(CUtensorMap* map, const void* base, bool words, uint64_t inner, uint64_t rows, uint64_t stride_bytes,
               uint32_t box_inner, uint32_t box_rows);

@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0, issued = 0, parity = 0;
-      bool ok = true;
+      bool ok = true, withhold = p.inject == 1 && blockIdx.x == 0;
       for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
         const int tm = t % tiles_m, tn = t / tiles_m;
         const int first_b = tn * BN / 128;
@@ -273,7 +273,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           issued |= 1u << stage;
           parity = (parity & ~(1u << stage)) | (phase << stage);
           const uint32_t a = smem0 + stage * C::kStageBytes, b = a + C::kABytes, sa = b + C::kBBytes, sb = sa + C::kScaleA;
-          tma_load_2d(a, &p.a, full_bar(stage), it * 128, tm * BM);
+          if (!withhold) tma_load_2d(a, &p.a, full_bar(stage), it * 128, tm * BM);
+          withhold = false;
           tma_load_2d(b, &p.b, full_bar(stage), it * 128, tn * BN);
           bulk_load(sa, static_cast<const uint8_t*>(p.a_scales) + (static_cast<long long>(tm) * ktiles + 2 * it) * kScaleTile,
                     sbytes, full_bar(stage));
@@ -523,7 +524,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0, issued = 0, parity = 0;
-      bool ok = true;
+      bool ok = true, withhold = p.inject == 1 && blockIdx.x == 0;
       for (int t = first; t < tiles && ok; t += npairs) {
         int tm, tn;
         tile_of(t, tiles_m, tiles_n, tm, tn);
@@ -541,7 +542,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t a = smem0 + stage * kStageBytes, b = a + kABytes, sa = b + kBBytes, sb = sa + kScaleA;
           tma_load_2d(sa, &p.sa, landed_bar(stage), it * 256, 2 * tm + rank);
           tma_load_2d(sb, &p.sb, landed_bar(stage), it * 256, 2 * tn);
-          tma_load_2d_pair(a, &p.a, fbar, it * 128, (2 * tm + rank) * BM);
+          if (!withhold) tma_load_2d_pair(a, &p.a, fbar, it * 128, (2 * tm + rank) * BM);
+          withhold = false;
           tma_load_2d_pair(b, &p.b, fbar, it * 128, tn * BN + rank * (BN / 2));
           if (++stage == S) {
             stage = 0;
@@ -743,7 +745,7 @@ cudaError_t launch_one(const ProductParams& p, int sms, cudaStream_t s) {
 
 template <typename T>
 cudaError_t launch_typed(const ProductParams& p, int sms, cudaStream_t s) {
-  switch (product_tile_n(p.m, p.n, sms)) {
+  switch (product_tile_n(p.m, p.n, p.k, sms)) {
     case 256: return pair::launch<T>(p, sms, s);
     case 32: return p.transposed ? launch_one<32, T, true>(p, sms, s) : launch_one<32, T, false>(p, sms, s);
     case 64: return p.transposed ? launch_one<64, T, true>(p, sms, s) : launch_one<64, T, false>(p, sms, s);
@@ -754,15 +756,16 @@ cudaError_t launch_typed(const ProductParams& p, int sms, cudaStream_t s) {
 }  // namespace
 
 // 32 or 64 where the smaller side has so few rows.  Else 256 (pairs of CTAs) or
-// 128 (one), whichever needs less time for its waves of tiles: a step of 64
-// along k takes a pair 128 cycles, and a CTA with its own 128 x 128 tile about
-// 80 (its shared memory, read at 128 bytes a cycle, bounds it, not the products).
-int product_tile_n(int m, int n, int sms) {
+// 128 (one CTA), whichever takes less time: measured, about 6.3 us + 0.35 us a
+// wave and stage along k for pairs, 4.2 us + 0.59 us for single CTAs (512 x 512 x
+// 1024: 7.7 against 6.5 us; x 8192: 17.5 against 22.9; 2048^3: 9.5 against 14.6).
+int product_tile_n(int m, int n, int k, int sms) {
   if (n <= 64) return n <= 32 ? 32 : 64;
   auto waves = [](long long tiles, long long at_once) { return (tiles + at_once - 1) / at_once; };
   const long long pairs = waves(static_cast<long long>((m + 255) / 256) * ((n + 255) / 256), sms / 2);
   const long long single = waves(static_cast<long long>((m + 127) / 128) * ((n + 127) / 128), sms);
-  return pairs * 128 <= single * 80 ? 256 : 128;
+  const long long stages = (k + kStageK - 1) / kStageK;
+  return 210 + 35 * pairs * stages <= 59 * single * stages ? 256 : 128;
 }
 
 cudaError_t launch_product(const ProductParams& p, int dtype, int sms, cudaStream_t s) {

@@ -37,8 +37,10 @@ def _on_stream(body, tensors, stream):
             stream = torch.cuda.ExternalStream(int(stream), device=index)
         elif stream.device.index != index:
             raise ValueError("stream belongs to another device than the tensors")
+        if stream.cuda_stream == torch.cuda.current_stream(index).cuda_stream:
+            return body(stream.cuda_stream)
         with torch.cuda.stream(stream):
-            for t in tensors:
+            for t in tensors:  # made on another stream, as far as the allocator knows
                 t.record_stream(stream)
             return body(stream.cuda_stream)
 
@@ -308,6 +310,26 @@ def _mx(q, name):
         raise ValueError(f"{name} must be a CUDA matrix")
 
 
+def _marshal_quantize(xs, sizes, row, col):
+    """muon_mx_quantize's host arrays, made once: returns call(raw stream).  ``row`` and ``col``: the
+    forms' (data, scales) addresses, or empty."""
+    values = array("q", [t.data_ptr() for t in xs])
+    values.extend([v for r, c, _ in sizes for v in (r, c)])
+    values.extend([ld for _, _, ld in sizes])
+    for pairs in (row, col):
+        values.extend([d for d, _ in pairs])
+        values.extend([q for _, q in pairs])
+    count, n, p = len(xs), 8 * len(xs), values.buffer_info()[0]
+    rd = p + 4 * n if row else None
+    cd = p + (6 if row else 4) * n if col else None
+    dtype, fn = _DTYPES[xs[0].dtype], _lib.lib().muon_mx_quantize
+
+    def call(s, values=values):  # keeps the arrays
+        check(fn(count, p, p + n, p + 3 * n, dtype, rd, rd and rd + n, cd, cd and cd + n, s))
+
+    return call
+
+
 def muon_mx_quantize(x, rows=True, cols=False, out=None, stream=None):
     """4-bit forms of a matrix, or of a list of matrices in one launch.
 
@@ -369,15 +391,7 @@ def muon_mx_quantize(x, rows=True, cols=False, out=None, stream=None):
             base = 0
             row = [f[0]._pointers() for f in given] if rows else []
             col = [f[-1]._pointers() for f in given] if cols else []
-        values = array("q", [t.data_ptr() for t in xs])
-        values.extend([v for r, c, _ in sizes for v in (r, c)])
-        values.extend([ld for _, _, ld in sizes])
-        for pairs in (row, col):
-            values.extend([base + d for d, _ in pairs])
-            values.extend([base + q for _, q in pairs])
-        n, p = 8 * len(xs), values.buffer_info()[0]
-        rd, cd = (p + 4 * n if rows else None), (p + (6 * n if rows else 4 * n) if cols else None)
-        check(_lib.lib().muon_mx_quantize(len(xs), p, p + n, p + 3 * n, _DTYPES[dtype], rd, rd and rd + n, cd, cd and cd + n, s))
+        _marshal_quantize(xs, sizes, [(base + d, base + q) for d, q in row], [(base + d, base + q) for d, q in col])(s)
         if out is not None:
             return out
         return forms[0] if single else forms

@@ -150,3 +150,46 @@ def test_mx_matrix_checks_its_tensors():
         nsb.muon_mx_product(e, e)
     with pytest.raises(ValueError):
         nsb.muon_mx_dequantize(e)
+
+
+def test_one_device_for_all_tensors():
+    from newton_schulz_12_b200 import layers
+
+    class Fake:
+        def __init__(self, index):
+            self.index = index
+
+        def get_device(self):
+            return self.index
+
+    with pytest.raises(ValueError, match="one device"):
+        layers._on_stream(lambda s: pytest.fail("called"), [Fake(0), Fake(1)], None)
+
+
+def test_tensors_of_another_device_than_the_current_one(monkeypatch):
+    """The call runs with the tensors' device current, on that device's current stream."""
+    import contextlib
+
+    from newton_schulz_12_b200 import layers
+    seen = []
+
+    class Fake:
+        def get_device(self):
+            return 1
+
+        def record_stream(self, s):
+            seen.append("recorded")
+
+    class Stream:
+        cuda_stream = 77
+
+    @contextlib.contextmanager
+    def device(index):
+        seen.append(("device", index))
+        yield
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda index=None: Stream())
+    assert layers._on_stream(lambda s: s, [Fake()], None) == 77
+    assert seen == [("device", 1)]
