@@ -233,14 +233,18 @@ class MxMatrix:
 
     def __init__(self, data, scales, rows, cols):
         rows, cols = int(rows), int(cols)
-        for t, name, shape in ((data, "data", self._data_shape(rows, cols)), (scales, "scales", self._scales_shape(rows, cols))):
-            if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8:
-                raise ValueError(f"{name} must be a uint8 tensor")
-            if t.shape != shape or not t.is_contiguous():
-                raise ValueError(f"{name} of a {rows} x {cols} matrix must be contiguous, {shape}, got {tuple(t.shape)}")
+        self._check(data, "data", self._data_shape(rows, cols), rows, cols)
+        self._check(scales, "scales", self._scales_shape(rows, cols), rows, cols)
         if scales.get_device() != data.get_device():
             raise ValueError("data and scales must be on one device")
         self.rows, self.cols, self._buffer, self._data, self._scales, self._at = rows, cols, None, data, scales, None
+
+    @staticmethod
+    def _check(t, name, shape, rows, cols):
+        if not isinstance(t, torch.Tensor) or t.dtype is not torch.uint8:
+            raise ValueError(f"{name} must be a uint8 tensor")
+        if t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name} of a {rows} x {cols} matrix must be contiguous, {shape}, got {tuple(t.shape)}")
 
     @staticmethod
     def _data_shape(rows, cols):
@@ -330,6 +334,29 @@ def _marshal_quantize(xs, sizes, row, col):
     return call
 
 
+def _quantize_one(x, rows, cols, stream):
+    """New forms of one matrix, with few steps: a token's call is as long as its Python."""
+    r, c, ld = _matrix(x, "x")
+
+    def body(s):
+        tiles = ((r + 127) >> 7) * ((c + 127) >> 7) * 512
+        rdata, cdata = r * ((c + 31) >> 5) * 16, c * ((r + 31) >> 5) * 16
+        second = rdata + tiles if rows else 0
+        buffer = torch.empty(second + cdata + tiles if cols else second, dtype=torch.uint8, device=x.device)
+        b = buffer.data_ptr()
+        values = array("q", (x.data_ptr(), r, c, ld, b, b + rdata, b + second, b + second + cdata))
+        v = values.buffer_info()[0]
+        check(_lib.lib().muon_mx_quantize(
+            1, v, v + 8, v + 24, _DTYPES[x.dtype], v + 32 if rows else None, v + 40 if rows else None,
+            v + 48 if cols else None, v + 56 if cols else None, s))
+        if not cols:
+            return MxMatrix._within(buffer, 0, r, c)
+        col = MxMatrix._within(buffer, second, c, r)
+        return (MxMatrix._within(buffer, 0, r, c), col) if rows else col
+
+    return _on_stream(body, [x], stream)
+
+
 def muon_mx_quantize(x, rows=True, cols=False, out=None, stream=None):
     """4-bit forms of a matrix, or of a list of matrices in one launch.
 
@@ -340,10 +367,12 @@ def muon_mx_quantize(x, rows=True, cols=False, out=None, stream=None):
     the one form or the pair ``(row form, column form)``; ``out`` of the same
     structure is written in place of new ones.
     """
-    single = isinstance(x, torch.Tensor)
-    xs = [x] if single else list(x)
     if not rows and not cols:
         raise ValueError("no form is wanted: rows or cols must be true")
+    single = isinstance(x, torch.Tensor)
+    if single and out is None:
+        return _quantize_one(x, rows, cols, stream)
+    xs = [x] if single else list(x)
     if not xs:
         return []
     dtype = xs[0].dtype if isinstance(xs[0], torch.Tensor) else None
@@ -392,9 +421,7 @@ def muon_mx_quantize(x, rows=True, cols=False, out=None, stream=None):
             row = [f[0]._pointers() for f in given] if rows else []
             col = [f[-1]._pointers() for f in given] if cols else []
         _marshal_quantize(xs, sizes, [(base + d, base + q) for d, q in row], [(base + d, base + q) for d, q in col])(s)
-        if out is not None:
-            return out
-        return forms[0] if single else forms
+        return forms if out is None else out
 
     return _on_stream(body, tensors, stream)
 
