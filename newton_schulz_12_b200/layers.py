@@ -438,30 +438,35 @@ def muon_mx_dequantize(q, dtype=torch.bfloat16, stream=None):
         raise ValueError(f"dtype must be bf16, fp16 or fp32, got {dtype}")
     if not qs:
         return []
-    tensors = {}
+    tensors, last = [], None
     for m in qs:
-        _mx(m, "q")
-        for t in m._tensors():
-            tensors[id(t)] = t
+        if not isinstance(m, MxMatrix) or m._buffer is None or m._buffer is not last:  # one check for each buffer
+            _mx(m, "q")
+            tensors += m._tensors()
+            last = m._buffer
 
     def body(s):
-        if single:
-            ys = [torch.empty(q.rows, q.cols, dtype=dtype, device=q.device)]
-        else:  # one allocation, each matrix on a 16-byte boundary
-            step = 16 // dtype.itemsize
-            spans = [-(-m.rows * m.cols // step) * step for m in qs]
-            parts = torch.empty(sum(spans), dtype=dtype, device=qs[0].device).split(spans)
-            ys = [(t if n == m.rows * m.cols else t[: m.rows * m.cols]).view(m.rows, m.cols) for t, n, m in zip(parts, spans, qs)]
-        places = [m._pointers() for m in qs]
-        values = array("q", [d for d, _ in places])
-        values.extend([q for _, q in places])
-        values.extend([v for m in qs for v in (m.rows, m.cols)])
-        values.extend([y.data_ptr() for y in ys])
+        # one allocation, each matrix on a 16-byte boundary
+        size = dtype.itemsize
+        unit = 16 // size
+        at, places, data, scales, shapes = 0, [], [], [], []
+        for m in qs:
+            r, c = m.rows, m.cols
+            places.append((at, r, c))
+            at += -(-r * c // unit) * unit
+            d, q = m._pointers()
+            data.append(d)
+            scales.append(q)
+            shapes += (r, c)
+        flat = torch.empty(at, dtype=dtype, device=tensors[0].device)
+        base, strided = flat.data_ptr(), flat.as_strided
+        values = array("q", data + scales + shapes + [base + size * o for o, _, _ in places])
         n, p = 8 * len(qs), values.buffer_info()[0]
         check(_lib.lib().muon_mx_dequantize(len(qs), p, p + n, p + 2 * n, p + 4 * n, _DTYPES[dtype], s))
+        ys = [strided((r, c), (c, 1), o) for o, r, c in places]
         return ys[0] if single else ys
 
-    return _on_stream(body, list(tensors.values()), stream)
+    return _on_stream(body, tensors, stream)
 
 
 def muon_mx_product(a, b, dtype=torch.bfloat16, out=None, stream=None):
