@@ -23,10 +23,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ float as_float(float v) { return v; }
-__device__ __forceinline__ float as_float(bf16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float as_float(__half v) { return __half2float(v); }
-
 template <typename T>
 __device__ __forceinline__ T rounded(float v);
 template <>
@@ -63,9 +59,19 @@ __device__ __forceinline__ uint32_t encode8(const float* v, float inv = 1.f) {
 }
 
 // Two 16-bit values of one word: the larger magnitudes of two words side by
-// side (as integers: they order alike, infinities and NaNs above all), and the
-// fp32 bits of a magnitude.
-__device__ __forceinline__ uint32_t max_magnitudes(uint32_t a, uint32_t w) { return __vmaxu2(a, w & 0x7FFF7FFFu); }
+// side (a NaN stays one), and the fp32 bits of a magnitude.
+template <typename T>
+__device__ __forceinline__ uint32_t max_magnitudes(uint32_t a, uint32_t w);
+template <>
+__device__ __forceinline__ uint32_t max_magnitudes<bf16>(uint32_t a, uint32_t w) {
+  const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+template <>
+__device__ __forceinline__ uint32_t max_magnitudes<__half>(uint32_t a, uint32_t w) {
+  const __half2 r = __hmax2_nan(*reinterpret_cast<const __half2*>(&a), __habs2(*reinterpret_cast<const __half2*>(&w)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 template <typename T>
 __device__ __forceinline__ uint32_t magnitude_bits(uint32_t half);
 template <>
@@ -149,12 +155,19 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
   } else {
     constexpr int kBatch = 16;
     const int c = threadIdx.x & 127, half = threadIdx.x >> 7;
+    const bool full = rows == kTile && cols == kTile;
     for (int b = half; b < kTile; b += 2 * kBatch) {
       T v[kBatch];
+      if (full) {
+        const T* at = x + b * M.ldx + c;
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int r = b + 2 * i;
-        v[i] = r < rows && c < cols ? x[r * M.ldx + c] : rounded<T>(0.f);
+        for (int i = 0; i < kBatch; ++i) v[i] = at[2 * i * M.ldx];
+      } else {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int r = b + 2 * i;
+          v[i] = r < rows && c < cols ? x[r * M.ldx + c] : rounded<T>(0.f);
+        }
       }
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) tile[(b + 2 * i) * kTile + c] = v[i];
@@ -174,7 +187,7 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
       if constexpr (sizeof(T) == 2) {
         const uint32_t* w = reinterpret_cast<const uint32_t*>(&e);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) amax = max_magnitudes(amax, w[k]);
+        for (int k = 0; k < 4; ++k) amax = max_magnitudes<T>(amax, w[k]);
         amax = max(amax & 0xFFFFu, amax >> 16);
         // four threads hold a block
         amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
@@ -215,7 +228,7 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
 #pragma unroll
       for (int k = 0; k < 32; ++k) {
         w[k] = src[k * (kTile / 2)];
-        amax = max_magnitudes(amax, w[k]);
+        amax = max_magnitudes<T>(amax, w[k]);
       }
       const uint32_t b0 = scale_byte(magnitude_bits<T>(amax & 0xFFFFu)), b1 = scale_byte(magnitude_bits<T>(amax >> 16));
       const float i0 = inverse_scale(b0), i1 = inverse_scale(b1);
