@@ -185,6 +185,18 @@ def test_given_streams_and_threads():
         assert same(got[i], want[i])
 
 
+def test_the_default_stream_by_its_handle():
+    x, dy, w, b, W = make(100, 128, 256, seed=20)
+    Wr, Wc = nsb.muon_mx_quantize(W, rows=True, cols=True)
+    want = step(x, dy, w, b, Wr, Wc)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        got = step(x, dy, w, b, Wr, Wc, stream=torch.cuda.default_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert same(got, want)
+
+
 def test_more_than_32_bits_of_offsets():
     """Matrices of more than 2^31 values: the last rows as by themselves."""
     rows, cols = (1 << 21) + 77, 1032

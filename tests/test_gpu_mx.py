@@ -88,6 +88,26 @@ def test_quantize_special_values():
     assert np.array_equal(v[~np.isnan(v)], want[~np.isnan(want)])
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_quantize_special_values_of_16_bits(dtype):
+    """Subnormals, ties, the largest values, infinities and NaNs in blocks of every alignment."""
+    info = torch.finfo(dtype)
+    sub = info.smallest_normal * info.eps  # the smallest subnormal
+    x = torch.zeros(64, 96, dtype=torch.float64)
+    x[0] = sub * (torch.arange(96) % 7)
+    x[1] = info.smallest_normal * (1 + (torch.arange(96) % 5) * info.eps)
+    x[2, ::2], x[2, 1::2] = info.max, -info.max / 3
+    x[3] = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0] * 12) * info.smallest_normal * 4
+    x[4] = -x[3]
+    x[5, 40], x[6, 41], x[7, 0] = float("inf"), float("nan"), -float("inf")
+    x[8, 3], x[8, 4:32] = 1.0, sub
+    x[40:] = torch.randn(24, 96, generator=torch.Generator().manual_seed(1)) * sub * 100
+    x = x.to(dtype).cuda()
+    row, col = nsb.muon_mx_quantize(x, rows=True, cols=True)
+    check_form(row, host(x))
+    check_form(col, host(x).T)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_dequantize(dtype):
     xs = [normal(s, 40 + i, torch.float32, 1.0).cuda() for i, s in enumerate(SHAPES)]
@@ -157,12 +177,13 @@ def test_product(m, n, k):
     assert nsb.muon_get_status() == 0
 
 
-def test_product_scales_far_apart():
+@pytest.mark.parametrize("m,n", [(200, 150), (20, 300), (300, 60), (2100, 2300)])
+def test_product_scales_far_apart(m, n):
     """Each block its own scale, over many powers of two: every scale byte reaches its own block."""
     g = torch.Generator().manual_seed(9)
-    x = torch.randn(200, 640, generator=g).view(200, 20, 32) * 2.0 ** torch.randint(-12, 12, (200, 20, 1), generator=g)
-    y = torch.randn(150, 640, generator=g).view(150, 20, 32) * 2.0 ** torch.randint(-12, 12, (150, 20, 1), generator=g)
-    a, b = nsb.muon_mx_quantize([x.reshape(200, 640).cuda(), y.reshape(150, 640).cuda()])
+    x = torch.randn(m, 640, generator=g).view(m, 20, 32) * 2.0 ** torch.randint(-12, 12, (m, 20, 1), generator=g)
+    y = torch.randn(n, 640, generator=g).view(n, 20, 32) * 2.0 ** torch.randint(-12, 12, (n, 20, 1), generator=g)
+    a, b = nsb.muon_mx_quantize([x.reshape(m, 640).cuda(), y.reshape(n, 640).cuda()])
     check_product(nsb.muon_mx_product(a, b, torch.float32), a, b, torch.float32)
 
 
