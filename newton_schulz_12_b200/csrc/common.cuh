@@ -34,6 +34,10 @@ __device__ __forceinline__ unsigned long long global_ns() {
   return t;
 }
 
+// Waits until the stream's previous kernel has ended and its writes are seen
+// (of kernels launched with launch_after; elsewhere it returns at once).
+__device__ __forceinline__ void previous_kernel_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }

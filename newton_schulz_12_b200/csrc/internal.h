@@ -454,6 +454,25 @@ cudaError_t take_captured_status(int* value);
 
 }  // namespace mx
 
+// A launch whose blocks may be set up while the stream's previous kernel drains:
+// the kernel waits for that one's end (previous_kernel_done) before it touches
+// memory.  Saves 1 to 3 us a kernel (32768 x 768 bf16 norm in a row of others:
+// 24.2 -> 22.0 us; its gradient, two kernels: 34.8 -> 31.4 us).
+template <typename... Params, typename... Args>
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s, const Args&... args) {
+  cudaLaunchAttribute early = {};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ------------------------------------------------ shared by the C-ABI files
 namespace host {
 

@@ -62,6 +62,7 @@ __device__ __forceinline__ float block_sum(float v, float* buf) {
 // alignment.
 template <typename T, typename P>
 __global__ void __launch_bounds__(kLoopThreads) forward_loop_kernel(const FwdParams p) {
+  previous_kernel_done();
   __shared__ float buf[32];
   for (long long r = blockIdx.x; r < p.rows; r += gridDim.x) {
     const T* x = static_cast<const T*>(p.x) + r * p.ldx;
@@ -91,6 +92,7 @@ __global__ void __launch_bounds__(kLoopThreads) forward_loop_kernel(const FwdPar
 // dx of one row a block at a time, read twice.
 template <typename T, typename P>
 __global__ void __launch_bounds__(kLoopThreads) backward_loop_kernel(const BwdParams p) {
+  previous_kernel_done();
   __shared__ float buf[32];
   for (long long r = blockIdx.x; r < p.rows; r += gridDim.x) {
     const T* x = static_cast<const T*>(p.x) + r * p.ldx;
@@ -118,6 +120,7 @@ __global__ void __launch_bounds__(kLoopThreads) backward_loop_kernel(const BwdPa
 // dw and db from the partials, summed in a fixed order; 32 columns a block.
 template <typename P>
 __global__ void __launch_bounds__(1024) finish_kernel(const BwdParams p) {
+  previous_kernel_done();
   __shared__ float sw[32][33], sb[32][33];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + tx;
@@ -186,6 +189,7 @@ struct __align__(16) Pack {
 // j-th of `parts` runs of rows, and writes partial j.
 template <typename T, int V>
 __global__ void __launch_bounds__(256) column_kernel(const BwdParams p) {
+  previous_kernel_done();
   __shared__ float part[8][32 * V + 1];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int c = (blockIdx.x * 32 + tx) * V;
@@ -479,6 +483,7 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float (*buf)[32], int t
 // the parameters.
 template <typename T, typename P, int VEC, int NV, int R, bool RING>
 __global__ void __launch_bounds__(kFwdThreads) forward_kernel(const FwdParams p, int tpr, int groups, int depth) {
+  previous_kernel_done();
   constexpr int E = VEC * NV;
   __shared__ float buf[2][R][32];
   extern __shared__ __align__(16) uint8_t smem[];
@@ -597,6 +602,7 @@ __global__ void __launch_bounds__(kFwdThreads) forward_kernel(const FwdParams p,
 // add nothing; rows beyond the matrix have rstd 0.
 template <typename T, typename P, int VEC, int NV, int R, bool SUMS, bool RING>
 __global__ void __launch_bounds__(SUMS ? kBwdThreads : kFwdThreads) backward_kernel(const BwdParams p, int tpr, int groups, int depth) {
+  previous_kernel_done();
   constexpr int E = VEC * NV;
   __shared__ float buf[2][2 * R][32];
   extern __shared__ __align__(16) uint8_t smem[];
@@ -819,9 +825,8 @@ cudaError_t forward_with(const FwdParams& p, const Shape& h, int sms, cudaStream
       threads, RING ? threads * R * Ring<T, VEC, NV>::kRow : 0, RING ? 2 * VEC * NV * h.tpr * 4 : 0, 0, &f);
   if (e != cudaSuccess) return e;
   const long long want = (p.rows + h.groups * R - 1) / (h.groups * R), most = static_cast<long long>(sms) * f.blocks;
-  forward_kernel<T, P, VEC, NV, R, RING>
-      <<<static_cast<int>(want < most ? want : most), threads, f.smem, s>>>(p, h.tpr, h.groups, f.depth);
-  return cudaGetLastError();
+  return launch_after(forward_kernel<T, P, VEC, NV, R, RING>, static_cast<int>(want < most ? want : most), threads, f.smem, s, p,
+                      h.tpr, h.groups, f.depth);
 }
 
 // Rows enough for the ring: four or more a group.
@@ -847,7 +852,9 @@ template <typename T, typename P>
 cudaError_t forward(const FwdParams& p, int sms, cudaStream_t s) {
   constexpr int V = 16 / static_cast<int>(sizeof(T));
   const bool vec = p.cols % V == 0 && aligned_rows<T>(p.x, p.ldx, p.rows) && aligned_rows<T>(p.y, p.ldy, p.rows);
-  const Shape h = shape_of(p.rows, p.cols, sms, vec || p.cols > kFwdE / 2 * kFwdThreads ? kFwdE : kFwdE / 2, kFwdThreads);
+  // one-value accesses leave fewer registers
+  const int max_e = vec || p.cols > 24 * kFwdThreads ? kFwdE : p.cols > 16 * kFwdThreads ? 24 : 16;
+  const Shape h = shape_of(p.rows, p.cols, sms, max_e, kFwdThreads);
   switch (h.e) {
     case 8: return vec ? forward_as<T, P, V, 8 / V>(p, h, sms, s) : forward_as<T, P, 1, 8>(p, h, sms, s);
     case 16: return vec ? forward_as<T, P, V, 16 / V>(p, h, sms, s) : forward_as<T, P, 1, 16>(p, h, sms, s);
@@ -855,8 +862,7 @@ cudaError_t forward(const FwdParams& p, int sms, cudaStream_t s) {
     case 32: return vec ? forward_as<T, P, V, 32 / V>(p, h, sms, s) : forward_as<T, P, 1, 32>(p, h, sms, s);
   }
   const long long want = static_cast<long long>(sms) * 4;
-  forward_loop_kernel<T, P><<<static_cast<int>(p.rows < want ? p.rows : want), kLoopThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_after(forward_loop_kernel<T, P>, static_cast<int>(p.rows < want ? p.rows : want), kLoopThreads, 0, s, p);
 }
 
 // Blocks of a backward launch that also adds up the columns: as many threads
@@ -888,8 +894,8 @@ cudaError_t backward_with(const BwdParams& p, const Shape& h, int sms, cudaStrea
   if (e != cudaSuccess) return e;
   long long blocks = SUMS ? column_blocks(p.rows, h, sms) : p.rows;
   if (!SUMS && blocks > static_cast<long long>(sms) * f.blocks) blocks = static_cast<long long>(sms) * f.blocks;
-  backward_kernel<T, P, VEC, NV, R, SUMS, RING><<<static_cast<int>(blocks), threads, f.smem, s>>>(p, h.tpr, h.groups, f.depth);
-  return cudaGetLastError();
+  return launch_after(backward_kernel<T, P, VEC, NV, R, SUMS, RING>, static_cast<int>(blocks), threads, f.smem, s, p, h.tpr,
+                      h.groups, f.depth);
 }
 
 template <typename T, typename P, int VEC, int NV, bool SUMS>
@@ -926,19 +932,16 @@ cudaError_t backward(BwdParams p, int sms, cudaStream_t s) {
       e = vec ? backward_as<T, P, V, 32 / V, false>(p, h, sms, s) : backward_as<T, P, 1, 32, false>(p, h, sms, s);
     else {
       const long long want = static_cast<long long>(sms) * 4;
-      backward_loop_kernel<T, P><<<static_cast<int>(p.rows < want ? p.rows : want), kLoopThreads, 0, s>>>(p);
-      e = cudaGetLastError();
+      e = launch_after(backward_loop_kernel<T, P>, static_cast<int>(p.rows < want ? p.rows : want), kLoopThreads, 0, s, p);
     }
   }
   if (e != cudaSuccess || !(p.dweight || p.dbias)) return e;
   if (!held && p.parts > 0) {
-    if (vec)
-      column_kernel<T, V><<<dim3((p.cols + 32 * V - 1) / (32 * V), p.parts), 256, 0, s>>>(p);
-    else
-      column_kernel<T, 1><<<dim3((p.cols + 31) / 32, p.parts), 256, 0, s>>>(p);
+    e = vec ? launch_after(column_kernel<T, V>, dim3((p.cols + 32 * V - 1) / (32 * V), p.parts), 256, 0, s, p)
+            : launch_after(column_kernel<T, 1>, dim3((p.cols + 31) / 32, p.parts), 256, 0, s, p);
+    if (e != cudaSuccess) return e;
   }
-  finish_kernel<P><<<(p.cols + 31) / 32, 1024, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_after(finish_kernel<P>, (p.cols + 31) / 32, 1024, 0, s, p);
 }
 
 }  // namespace

@@ -199,6 +199,7 @@ __device__ __forceinline__ void store_chunk(T* out, const ProductParams& p, cons
 
 template <int BN, typename T, bool TRANS>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ ProductParams p) {
+  previous_kernel_done();
   using C = Cfg<BN>;
   constexpr int S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -458,6 +459,7 @@ __device__ __forceinline__ void tile_of(int t, int tiles_m, int tiles_n, int& tm
 template <typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     pair_kernel(const __grid_constant__ ProductParams p) {
+  previous_kernel_done();
   using C = Cfg<T>;
   constexpr int S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -721,8 +723,7 @@ cudaError_t launch(const ProductParams& p, int sms, cudaStream_t s) {
   long long pairs = sms / 2;
   if (resident > 0 && pairs > resident) pairs = resident;
   if (pairs > tiles) pairs = tiles;
-  pair_kernel<T><<<static_cast<int>(2 * pairs), kThreads, Cfg<T>::kSmem, s>>>(p);
-  return cudaGetLastError();
+  return launch_after(pair_kernel<T>, static_cast<int>(2 * pairs), kThreads, Cfg<T>::kSmem, s, p);
 }
 
 }  // namespace pair
@@ -739,8 +740,7 @@ cudaError_t launch_one(const ProductParams& p, int sms, cudaStream_t s) {
     configured_device = dev;
   }
   const long long tiles = static_cast<long long>((p.m + BM - 1) / BM) * ((p.n + BN - 1) / BN);
-  product_kernel<BN, T, TRANS><<<static_cast<int>(tiles < sms ? tiles : sms), kThreads, Cfg<BN>::kSmem, s>>>(p);
-  return cudaGetLastError();
+  return launch_after(product_kernel<BN, T, TRANS>, static_cast<int>(tiles < sms ? tiles : sms), kThreads, Cfg<BN>::kSmem, s, p);
 }
 
 template <typename T>

@@ -122,6 +122,7 @@ struct __align__(16) Eight {
 // reads it in another order.
 template <typename T, bool VEC, bool COLS>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constant__ QuantParams p) {
+  previous_kernel_done();
   extern __shared__ __align__(16) uint8_t smem[];
   T* tile = reinterpret_cast<T*>(smem);                                // COLS or !VEC: [kTile][kTile]
   uint4* codes = reinterpret_cast<uint4*>(tile + kTile * kTile);       // COLS: [column][4 blocks]
@@ -298,6 +299,7 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
 // stores of single values lie side by side.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) dequantize_kernel(const __grid_constant__ DequantParams p) {
+  previous_kernel_done();
   extern __shared__ __align__(16) uint8_t smem[];
   const DequantMat& M = p.mat[matrix_of(p, blockIdx.x)];
   const int local = blockIdx.x - M.tile_begin;
@@ -360,8 +362,7 @@ cudaError_t quantize_as(const QuantParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
-  quantize_kernel<T, VEC, COLS><<<p.ntiles, kThreads, smem, s>>>(p);
-  return cudaGetLastError();
+  return launch_after(quantize_kernel<T, VEC, COLS>, p.ntiles, kThreads, smem, s, p);
 }
 
 // A launch reads eight values at once where all of its matrices allow it.
@@ -382,8 +383,7 @@ cudaError_t dequantize(const DequantParams& p, cudaStream_t s) {
   bool vec = true;
   for (int i = 0; i < p.nmat; ++i) vec = vec && p.mat[i].cols % 8 == 0 && reinterpret_cast<uintptr_t>(p.mat[i].y) % 16 == 0;
   if (vec) {
-    dequantize_kernel<T, true><<<p.ntiles, kThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_after(dequantize_kernel<T, true>, p.ntiles, kThreads, 0, s, p);
   }
   constexpr int smem = kTile * kTile * static_cast<int>(sizeof(T));
   static thread_local int configured_device = -1;
@@ -394,8 +394,7 @@ cudaError_t dequantize(const DequantParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
-  dequantize_kernel<T, false><<<p.ntiles, kThreads, smem, s>>>(p);
-  return cudaGetLastError();
+  return launch_after(dequantize_kernel<T, false>, p.ntiles, kThreads, smem, s, p);
 }
 
 }  // namespace

@@ -139,6 +139,28 @@ def test_quantize_into_given_forms():
     check_form(out[1], host(x).T)
 
 
+@pytest.mark.parametrize("shape", [(1, 1), (33, 65), (130, 257), (256, 128)])
+def test_nothing_beside_the_forms_is_written(shape):
+    """Forms and values between guard bytes."""
+    def guarded(count, dtype=torch.uint8):
+        wide = torch.full((count + 2 * 256,), 77, dtype=torch.uint8, device="cuda")
+        return wide, wide[256:256 + count].view(dtype)
+    r, c = shape
+    x = normal(shape, 6, torch.bfloat16).cuda()
+    wides, forms = [], []
+    for a, b in ((r, c), (c, r)):
+        d, s = nsb.MxMatrix._data_shape(a, b), nsb.MxMatrix._scales_shape(a, b)
+        wd, vd = guarded(d[0] * d[1])
+        ws, vs = guarded(s[0] * s[1] * 512)
+        wides += [wd, ws]
+        forms.append(nsb.MxMatrix(vd.view(d), vs.view(s), a, b))
+    nsb.muon_mx_quantize(x, rows=True, cols=True, out=tuple(forms))
+    check_form(forms[0], host(x))
+    check_form(forms[1], host(x).T)
+    for w in wides:
+        assert (w[:256] == 77).all() and (w[-256:] == 77).all()
+
+
 def exact_product(a, b):
     """C and sum |a||b| in fp64 from what the forms hold."""
     def val(q):
