@@ -4,6 +4,7 @@ The step of one hidden layer: h = layer_norm(x), y = Q(h) Q(W)^T, then from dy t
 muon_step takes), dx, dw, db, and the new weight's 4-bit forms.  Each stage is checked against its plain
 form on the values that the stage before it really gave.
 """
+import functools
 import threading
 
 import numpy as np
@@ -16,6 +17,12 @@ import newton_schulz_12_b200 as nsb
 pytestmark = pytest.mark.gpu
 
 U = 2.0 ** -24
+
+
+@functools.lru_cache(maxsize=None)
+def streams():
+    """Three streams for all tests here (torch hands out the same 32 in turn)."""
+    return [torch.cuda.Stream() for _ in range(3)]
 
 
 def host(x):
@@ -125,15 +132,14 @@ def test_two_graphs_replayed_side_by_side():
     forms = [nsb.muon_mx_quantize(W, rows=True, cols=True) for *_, W in sets]
     want = [step(*p[:4], *f) for p, f in zip(sets, forms)]
     torch.cuda.synchronize()
-    s, graphs, got = torch.cuda.Stream(), [], []
+    s, graphs, got = streams()[0], [], []
     for p, f in zip(sets, forms):
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g, stream=s):
             got.append(step(*p[:4], *f))
         graphs.append(g)
-    streams = [torch.cuda.Stream() for _ in graphs]
     for _ in range(20):
-        for g, st in zip(graphs, streams):
+        for g, st in zip(graphs, streams()[1:]):
             with torch.cuda.stream(st):
                 g.replay()
     torch.cuda.synchronize()
@@ -148,7 +154,7 @@ def test_plan_with_forms_captured():
     M = [torch.zeros(s, device="cuda") for s in shapes]
     W2, M2 = [w.clone() for w in W], [m.clone() for m in M]
     plan = nsb.MuonStepPlan(W, G, M, mx_forms=True)
-    plan.capture()
+    plan.capture(streams()[0])
     plan.replay()
     for _ in range(2):
         nsb.muon_step(W2, G, M2)
@@ -166,10 +172,11 @@ def test_given_streams_and_threads():
     want = [step(*p[:4], *f) for p, f in zip(sets, forms)]
     torch.cuda.synchronize()
     got, wrong = [None] * 4, []
+    streams()
 
     def work(i):
         try:
-            s = torch.cuda.Stream()
+            s = streams()[i % 3]
             for _ in range(10):
                 got[i] = step(*sets[i][:4], *forms[i], stream=s if i % 2 else s.cuda_stream)
             s.synchronize()
@@ -190,8 +197,7 @@ def test_the_default_stream_by_its_handle():
     Wr, Wc = nsb.muon_mx_quantize(W, rows=True, cols=True)
     want = step(x, dy, w, b, Wr, Wc)
     torch.cuda.synchronize()
-    s = torch.cuda.Stream()
-    with torch.cuda.stream(s):
+    with torch.cuda.stream(streams()[0]):
         got = step(x, dy, w, b, Wr, Wc, stream=torch.cuda.default_stream().cuda_stream)
     torch.cuda.synchronize()
     assert same(got, want)
