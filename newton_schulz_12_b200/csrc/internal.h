@@ -440,6 +440,7 @@ struct ProductParams {
   long long ldo;
   int m, n, k;
   int transposed;        // 1: a, m are the caller's B and n: out[col * ldo + row]
+  int split;             // CTAs that share a tile, each with a run of k (set by launch_product)
   int* status;
   unsigned long long timeout_ns;
   int inject;            // 1: withhold one operand copy in block 0 (timeout-path test)
@@ -458,18 +459,23 @@ cudaError_t take_captured_status(int* value);
 // the kernel waits for that one's end (previous_kernel_done) before it touches
 // memory.  Saves 1 to 3 us a kernel (32768 x 768 bf16 norm in a row of others:
 // 24.2 -> 22.0 us; its gradient, two kernels: 34.8 -> 31.4 us).
+// cluster: blocks a cluster, or 1 (a kernel's own cluster size stands).
 template <typename... Params, typename... Args>
-cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s, const Args&... args) {
-  cudaLaunchAttribute early = {};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s, int cluster,
+                         const Args&... args) {
+  cudaLaunchAttribute attrs[2] = {};
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  attrs[1].id = cudaLaunchAttributeClusterDimension;
+  attrs[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
+  cfg.attrs = attrs;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 

@@ -825,7 +825,7 @@ cudaError_t forward_with(const FwdParams& p, const Shape& h, int sms, cudaStream
       threads, RING ? threads * R * Ring<T, VEC, NV>::kRow : 0, RING ? 2 * VEC * NV * h.tpr * 4 : 0, 0, &f);
   if (e != cudaSuccess) return e;
   const long long want = (p.rows + h.groups * R - 1) / (h.groups * R), most = static_cast<long long>(sms) * f.blocks;
-  return launch_after(forward_kernel<T, P, VEC, NV, R, RING>, static_cast<int>(want < most ? want : most), threads, f.smem, s, p,
+  return launch_after(forward_kernel<T, P, VEC, NV, R, RING>, static_cast<int>(want < most ? want : most), threads, f.smem, s, 1, p,
                       h.tpr, h.groups, f.depth);
 }
 
@@ -862,7 +862,7 @@ cudaError_t forward(const FwdParams& p, int sms, cudaStream_t s) {
     case 32: return vec ? forward_as<T, P, V, 32 / V>(p, h, sms, s) : forward_as<T, P, 1, 32>(p, h, sms, s);
   }
   const long long want = static_cast<long long>(sms) * 4;
-  return launch_after(forward_loop_kernel<T, P>, static_cast<int>(p.rows < want ? p.rows : want), kLoopThreads, 0, s, p);
+  return launch_after(forward_loop_kernel<T, P>, static_cast<int>(p.rows < want ? p.rows : want), kLoopThreads, 0, s, 1, p);
 }
 
 // Blocks of a backward launch that also adds up the columns: as many threads
@@ -894,7 +894,7 @@ cudaError_t backward_with(const BwdParams& p, const Shape& h, int sms, cudaStrea
   if (e != cudaSuccess) return e;
   long long blocks = SUMS ? column_blocks(p.rows, h, sms) : p.rows;
   if (!SUMS && blocks > static_cast<long long>(sms) * f.blocks) blocks = static_cast<long long>(sms) * f.blocks;
-  return launch_after(backward_kernel<T, P, VEC, NV, R, SUMS, RING>, static_cast<int>(blocks), threads, f.smem, s, p, h.tpr,
+  return launch_after(backward_kernel<T, P, VEC, NV, R, SUMS, RING>, static_cast<int>(blocks), threads, f.smem, s, 1, p, h.tpr,
                       h.groups, f.depth);
 }
 
@@ -932,16 +932,16 @@ cudaError_t backward(BwdParams p, int sms, cudaStream_t s) {
       e = vec ? backward_as<T, P, V, 32 / V, false>(p, h, sms, s) : backward_as<T, P, 1, 32, false>(p, h, sms, s);
     else {
       const long long want = static_cast<long long>(sms) * 4;
-      e = launch_after(backward_loop_kernel<T, P>, static_cast<int>(p.rows < want ? p.rows : want), kLoopThreads, 0, s, p);
+      e = launch_after(backward_loop_kernel<T, P>, static_cast<int>(p.rows < want ? p.rows : want), kLoopThreads, 0, s, 1, p);
     }
   }
   if (e != cudaSuccess || !(p.dweight || p.dbias)) return e;
   if (!held && p.parts > 0) {
-    e = vec ? launch_after(column_kernel<T, V>, dim3((p.cols + 32 * V - 1) / (32 * V), p.parts), 256, 0, s, p)
-            : launch_after(column_kernel<T, 1>, dim3((p.cols + 31) / 32, p.parts), 256, 0, s, p);
+    e = vec ? launch_after(column_kernel<T, V>, dim3((p.cols + 32 * V - 1) / (32 * V), p.parts), 256, 0, s, 1, p)
+            : launch_after(column_kernel<T, 1>, dim3((p.cols + 31) / 32, p.parts), 256, 0, s, 1, p);
     if (e != cudaSuccess) return e;
   }
-  return launch_after(finish_kernel<P>, (p.cols + 31) / 32, 1024, 0, s, p);
+  return launch_after(finish_kernel<P>, (p.cols + 31) / 32, 1024, 0, s, 1, p);
 }
 
 }  // namespace

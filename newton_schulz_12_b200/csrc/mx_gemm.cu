@@ -1,13 +1,16 @@
 // C = A B^T of two 4-bit microscaled matrices on the tensor cores
 // (tcgen05.mma kind::mxf4, one scale byte for every 32 values along k).
 //
-// A CTA holds a 128 x BN tile of C in tensor memory.  Warp 0 copies the
-// operands' data (128-byte swizzled boxes of 128 bytes = 256 values along k)
-// and their scales (512-byte tiles of 128 rows x 4 blocks, already in the
-// order that tcgen05.cp wants) into a ring; one thread of warp 1 copies each
+// Small products: a CTA holds a 128 x BN tile of C in tensor memory.  Warp 0
+// copies the operands' data (128-byte swizzled boxes of 128 bytes = 256 values
+// along k) and their scales (512-byte tiles of 128 rows x 4 blocks, already in
+// the order that tcgen05.cp wants) into a ring; one thread of warp 1 copies each
 // stage's scales on to tensor memory and issues the products; four warps
 // convert and store the finished tile while the next one is computed in the
-// second accumulator.
+// second accumulator.  Where few tiles leave SMs idle (a token's row against a
+// whole weight), a cluster of CTAs shares a tile, each with a run of k, and adds
+// the partial sums up through distributed shared memory in rank order.
+// (Large products: namespace pair below.)
 #include "common.cuh"
 #include "internal.h"
 
@@ -29,25 +32,22 @@ __device__ int g_captured_status;
 
 template <int BN>
 struct Cfg {
-  static constexpr int kScaleTilesB = (BN + 127) / 128;
   static constexpr uint32_t kABytes = BM * 128;
   static constexpr uint32_t kBBytes = BN * 128;
-  static constexpr uint32_t kScaleA = 2 * kScaleTile;  // two tiles along k
-  static constexpr uint32_t kScaleB = 2 * kScaleTile * kScaleTilesB;
+  static constexpr uint32_t kScaleA = 2 * kScaleTile, kScaleB = 2 * kScaleTile;  // two tiles along k
   static constexpr uint32_t kStageBytes = kABytes + kBBytes + kScaleA + kScaleB;
-  static constexpr int kStages = 5;
+  static constexpr int kStages = BN == 128 ? 5 : BN == 64 ? 7 : 8;
   static constexpr uint32_t kStageRow = 64 * 4 + 16;  // staging row: 64 values, padded against bank conflicts
   static constexpr uint32_t kStagingWarp = 32 * kStageRow;
-  // full, empty per stage; tfull, tempty x 2; scale slots x 2; drain
-  static constexpr int kBars = 2 * kStages + 7;
+  static constexpr int kBars = 2 * kStages + 5;       // full, empty per stage; tfull, tempty x 2; drain
   static constexpr size_t kSmem = 1024 + kStages * kStageBytes + 4 * kStagingWarp + kBars * 8 + 16;
-  // tensor memory columns: two accumulators, then two slots of a stage's scales
+  // tensor memory columns: two accumulators, then a slot of scales for each stage
   static constexpr uint32_t kScaleCol = 2 * BN;
-  static constexpr uint32_t kColsA = 2 * 4, kColsB = 2 * 4 * kScaleTilesB;  // 4 columns a tile
-  static constexpr uint32_t kSlotCols = kColsA + kColsB;
-  static_assert(kScaleCol + 2 * kSlotCols <= 512, "tensor memory");
+  static constexpr uint32_t kSlotCols = 16;           // 4 columns a tile of scales: A's two, B's two
+  static_assert(kScaleCol + kStages * kSlotCols <= 512, "tensor memory");
   static_assert(kSmem <= 232448, "shared memory");
   static_assert(kStageBytes % 1024 == 0, "swizzled boxes start on 1 KiB");
+  static_assert(BM * (BN + 1) * 4 <= kStages * kStageBytes, "a tile's partial sums fit the ring");
 };
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* map, uint32_t bar, int c0, int c1) {
@@ -64,14 +64,18 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
+// Descriptors as two words: only the low one (the address) changes in the issue loop.
+constexpr uint32_t kOperandHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // 8-row groups 1 KiB apart, 128-byte swizzle
+constexpr uint32_t kOperandLo = 1u << 16;
 // One tile of scales (32 rows of 16 bytes) to four columns of tensor memory,
 // the same in each quarter of the lanes: row 32 j + i of the operand is byte
 // group j of lane i.
-__device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint32_t saddr) {
-  uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(128u >> 4) << 32;  // 8-row groups of 16-byte rows; no swizzle
-  d |= 1ull << 46;
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+constexpr uint32_t kScaleHi = (128u >> 4) | (1u << 14);  // 8-row groups of 16-byte rows, no swizzle
+__device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint32_t lo) {
+  asm volatile(
+      "{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
+      "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr), "r"(lo), "r"(kScaleHi)
+      : "memory");
 }
 
 // Instruction descriptor of kind::mxf4: E2M1 operands, power-of-two scales,
@@ -81,13 +85,14 @@ __host__ __device__ constexpr uint32_t idesc_mxf4(int m, int n, int id) {
          (1u << 23) | (static_cast<uint32_t>(m >> 7) << 27) | (static_cast<uint32_t>(id) << 29);
 }
 
-__device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
-                                         uint32_t accumulate) {
+template <int BN, int ID>
+__device__ __forceinline__ void mma_mxf4(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t sa, uint32_t sb, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
       "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+      "mov.b64 a, {%1, %7};\n\tmov.b64 b, {%2, %7};\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc_mxf4(BM, BN, ID)), "r"(sa), "r"(sb), "r"(accumulate), "r"(kOperandHi)
       : "memory");
 }
 
@@ -102,9 +107,6 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* map, 
       "l"(reinterpret_cast<uint64_t>(map)), "r"(cbar), "r"(c0), "r"(c1)
       : "memory");
 }
-// Descriptors as two words: only the low one (the address) changes in the issue loop.
-constexpr uint32_t kOperandHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // 8-row groups 1 KiB apart, 128-byte swizzle
-constexpr uint32_t kOperandLo = 1u << 16;
 // A warp's lane quarter of tensor memory, 8 or 16 columns from `taddr`, one word a lane and column.
 __device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
@@ -159,6 +161,18 @@ __device__ __forceinline__ bf16 rounded<bf16>(float v) { return __float2bfloat16
 template <>
 __device__ __forceinline__ __half rounded<__half>(float v) { return __float2half_rn(v); }
 
+// CTAs that share a tile of 128 x bn, bn 32 or 64: as many as find an SM and a
+// stage along k each, 8 at most (16 x 4096 x 4096: 13.0 -> 6.4 us, 1 x 8192 x
+// 8192: 22.2 -> 11.8 us.  Of 128 x 128 tiles the partial sums cost more than the
+// split gives: 1024^3 12 us against 6).
+int split_of(int m, int n, int k, int bn, int sms) {
+  const long long tiles = static_cast<long long>((m + BM - 1) / BM) * ((n + bn - 1) / bn);
+  const int stages = (k + kStageK - 1) / kStageK;
+  int c = 1;
+  while (c < 8 && tiles * c * 2 <= sms && c * 2 <= stages) c *= 2;
+  return c;
+}
+
 // A warp's 32 rows x CW columns from their staging rows to C, cut at its edges.
 template <typename T, int CW>
 __device__ __forceinline__ void store_chunk(T* out, const ProductParams& p, const uint8_t* stg, uint32_t stg_row, long long row0,
@@ -197,7 +211,8 @@ __device__ __forceinline__ void store_chunk(T* out, const ProductParams& p, cons
   }
 }
 
-template <int BN, typename T, bool TRANS>
+// SPLIT: one tile a cluster, each CTA a run of k; else the CTAs walk over the tiles.
+template <int BN, typename T, bool TRANS, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ ProductParams p) {
   previous_kernel_done();
   using C = Cfg<BN>;
@@ -214,8 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   auto empty_bar = [&](int s) { return bar0 + 8u * (S + s); };
   auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * S + a); };
   auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * S + 2 + a); };
-  auto slot_bar = [&](int a) { return bar0 + 8u * (2 * S + 4 + a); };
-  const uint32_t drain_bar = bar0 + 8u * (2 * S + 6);
+  const uint32_t drain_bar = bar0 + 8u * (2 * S + 4);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -225,7 +239,6 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
       mbar_init(tempty_bar(a), 4);
-      mbar_init(slot_bar(a), 1);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -251,38 +264,35 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   const int tiles_m = (p.m + BM - 1) / BM, tiles_n = (p.n + BN - 1) / BN;
   const int tiles = tiles_m * tiles_n;
   const int kiters = (p.k + kStageK - 1) / kStageK;
-  const int ktiles = (p.k + 127) / 128;        // scale tiles along k
-  const int rows_b = (p.n + 127) / 128;        // scale tiles along B's rows
+  const int ktiles = (p.k + 127) / 128;  // scale tiles along k
+  const int share = SPLIT ? p.split : 1, rank = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
+  const int first = blockIdx.x / share, stride = gridDim.x / share;
+  const int it0 = SPLIT ? kiters * rank / share : 0, it1 = SPLIT ? kiters * (rank + 1) / share : kiters;
 
   if (warp == 0) {
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0, issued = 0, parity = 0;
       bool ok = true, withhold = p.inject == 1 && blockIdx.x == 0;
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      for (int t = first; t < tiles && ok; t += stride) {
         const int tm = t % tiles_m, tn = t / tiles_m;
-        const int first_b = tn * BN / 128;
-        const int nb = min(C::kScaleTilesB, rows_b - first_b);
-        for (int it = 0; it < kiters; ++it) {
+        const uint8_t* sa0 = static_cast<const uint8_t*>(p.a_scales) + static_cast<long long>(tm) * ktiles * kScaleTile;
+        const uint8_t* sb0 = static_cast<const uint8_t*>(p.b_scales) + static_cast<long long>(tn * BN / 128) * ktiles * kScaleTile;
+        for (int it = it0; it < it1; ++it) {
           if (!mbar_wait(empty_bar(stage), phase ^ 1u, ctl)) {
             ok = false;
             break;
           }
-          const int kt = min(2, ktiles - 2 * it);  // scale tiles of this stage along k
-          const uint32_t sbytes = static_cast<uint32_t>(kt) * kScaleTile;
-          mbar_arrive_expect_tx(full_bar(stage), C::kABytes + C::kBBytes + sbytes * (1 + nb));
+          const uint32_t sbytes = static_cast<uint32_t>(min(2, ktiles - 2 * it)) * kScaleTile;  // this stage's, along k
+          mbar_arrive_expect_tx(full_bar(stage), C::kABytes + C::kBBytes + 2 * sbytes);
           issued |= 1u << stage;
           parity = (parity & ~(1u << stage)) | (phase << stage);
           const uint32_t a = smem0 + stage * C::kStageBytes, b = a + C::kABytes, sa = b + C::kBBytes, sb = sa + C::kScaleA;
           if (!withhold) tma_load_2d(a, &p.a, full_bar(stage), it * 128, tm * BM);
           withhold = false;
           tma_load_2d(b, &p.b, full_bar(stage), it * 128, tn * BN);
-          bulk_load(sa, static_cast<const uint8_t*>(p.a_scales) + (static_cast<long long>(tm) * ktiles + 2 * it) * kScaleTile,
-                    sbytes, full_bar(stage));
-          for (int j = 0; j < nb; ++j)
-            bulk_load(sb + j * 2 * kScaleTile,
-                      static_cast<const uint8_t*>(p.b_scales) + (static_cast<long long>(first_b + j) * ktiles + 2 * it) * kScaleTile,
-                      sbytes, full_bar(stage));
+          bulk_load(sa, sa0 + static_cast<long long>(2 * it) * kScaleTile, sbytes, full_bar(stage));
+          bulk_load(sb, sb0 + static_cast<long long>(2 * it) * kScaleTile, sbytes, full_bar(stage));
           if (++stage == S) {
             stage = 0;
             phase ^= 1u;
@@ -296,50 +306,45 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0) {
-      int stage = 0, acc = 0, slot = 0;
-      uint32_t phase = 0, acc_phase = 0, slot_phase = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true, ready = false;
+      const uint32_t a0 = kOperandLo | (smem0 >> 4), s0 = (smem0 + C::kABytes + C::kBBytes) >> 4;
+      for (int t = first; t < tiles && ok; t += stride) {
         if (!mbar_wait(tempty_bar(acc), acc_phase ^ 1u, ctl)) break;
         tc_fence_after();
         const uint32_t d = tmem + static_cast<uint32_t>(acc * BN);
         const uint32_t group = static_cast<uint32_t>((t / tiles_m) * BN % 128) / 32;  // first 32 rows of B in its scale tile
-        for (int it = 0; it < kiters; ++it) {
-          // the slot's scales were last read by the products of two stages ago
-          if (!mbar_wait(full_bar(stage), phase, ctl) || !mbar_wait(slot_bar(slot), slot_phase ^ 1u, ctl)) {
+        uint32_t accumulate = 0;
+        for (int it = it0; it < it1; ++it) {
+          // full again: the products that last read this stage's operands and scales are done
+          if (!ready && !mbar_wait(full_bar(stage), phase, ctl)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a = smem0 + stage * C::kStageBytes, b = a + C::kABytes, sa = b + C::kBBytes, sb = sa + C::kScaleA;
-          const uint32_t ta = tmem + C::kScaleCol + static_cast<uint32_t>(slot) * C::kSlotCols, tb = ta + C::kColsA;
-          const int steps = min(4, (p.k - it * kStageK + 63) / 64);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (2 * h >= steps) break;
-            scales_to_tmem(ta + 4 * h, sa + h * kScaleTile);
-#pragma unroll
-            for (int j = 0; j < C::kScaleTilesB; ++j)
-              scales_to_tmem(tb + (h * C::kScaleTilesB + j) * 4, sb + (2 * j + h) * kScaleTile);
+          const uint32_t off = static_cast<uint32_t>(stage) * (C::kStageBytes >> 4);
+          const uint32_t a = a0 + off, b = a + (C::kABytes >> 4), sa = s0 + off, sb = sa + (C::kScaleA >> 4);
+          const uint32_t ta = tmem + C::kScaleCol + static_cast<uint32_t>(stage) * C::kSlotCols, tb = ta + 8;
+          const uint32_t empty = empty_bar(stage);
+          const int left = p.k - it * kStageK;
+          scales_to_tmem(ta, sa);
+          scales_to_tmem(tb, sb);
+          if (left > 128) {
+            scales_to_tmem(ta + 4, sa + (kScaleTile >> 4));
+            scales_to_tmem(tb + 4, sb + (kScaleTile >> 4));
           }
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            if (kk >= steps) break;
-            const uint32_t h = kk >> 1;
-            mma_mxf4(d, sdesc_sw128(a + kk * 32, 16, 1024), sdesc_sw128(b + kk * 32, 16, 1024),
-                     idesc_mxf4(BM, BN, 2 * (kk & 1)), ta + 4 * h, tb + h * C::kScaleTilesB * 4 + group,
-                     (it | kk) != 0 ? 1u : 0u);
-          }
-          tc_commit(empty_bar(stage));
-          tc_commit(slot_bar(slot));
+          mma_mxf4<BN, 0>(d, a, b, ta, tb + group, accumulate);
+          accumulate = 1;
           if (++stage == S) {
             stage = 0;
             phase ^= 1u;
           }
-          if (++slot == 2) {
-            slot = 0;
-            slot_phase ^= 1u;
-          }
+          ready = mbar_test(full_bar(stage), phase);  // while the products are issued
+          if (left > 64) mma_mxf4<BN, 2>(d, a + 2, b + 2, ta, tb + group, 1);
+          if (left > 128) mma_mxf4<BN, 0>(d, a + 4, b + 4, ta + 4, tb + 4 + group, 1);
+          if (left > 192) mma_mxf4<BN, 2>(d, a + 6, b + 6, ta + 4, tb + 4 + group, 1);
+          tc_commit(empty);
         }
         if (!ok) break;
         tc_commit(tfull_bar(acc));
@@ -352,6 +357,22 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       mbar_wait_drain(drain_bar, 0, drain_ns > 1000000ull ? drain_ns : 1000000ull);
     }
     __syncwarp();
+  } else if constexpr (SPLIT) {
+    // this CTA's partial sums over the ring (all its products are done), in the order in which C is written
+    const int quarter = warp & 3, row = quarter * 32 + lane;
+    const bool ok = mbar_wait(tfull_bar(0), 0, ctl);
+    if (__all_sync(0xFFFFFFFFu, ok)) {
+      tc_fence_after();
+      float* part = reinterpret_cast<float*>(smem) + (TRANS ? row : row * (BN + 1));
+#pragma unroll
+      for (int c0 = 0; c0 < BN; c0 += 32) {
+        uint32_t r[32];
+        tmem_ld_32x32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(c0), r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) part[(c0 + j) * (TRANS ? BM : 1)] = __uint_as_float(r[j]);
+      }
+    }
   } else {
     const int quarter = warp & 3;
     uint8_t* stg = staging + quarter * C::kStagingWarp;
@@ -360,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     const bool vec = (reinterpret_cast<uintptr_t>(out) % 16 == 0) && (p.ldo % kVec == 0);
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+    for (int t = first; t < tiles; t += stride) {
       const int tm = t % tiles_m, tn = t / tiles_m;
       const bool ok = mbar_wait(tfull_bar(acc), acc_phase, ctl);
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
@@ -405,7 +426,56 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     }
   }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (SPLIT) {
+    cluster_sync();  // every CTA's partial sums are written
+    if (warp >= 2) {
+      // a CTA adds up every share-th column (TRANS) or row, the partial sums in
+      // rank order; four of them, or of a row's 32 columns, a thread at a time
+      T* out = static_cast<T*>(p.out);
+      const int tm = first % tiles_m, tn = first / tiles_m;
+      const int rows = min(static_cast<long long>(BM), p.m - static_cast<long long>(tm) * BM), cols = min(BN, p.n - tn * BN);
+      const long long row0 = static_cast<long long>(tm) * BM, col0 = static_cast<long long>(tn) * BN;
+      auto add_up = [&](const uint32_t (&at)[4], float (&v)[4]) {
+        for (int q = 0; q < share; ++q) {
+          const uint32_t base = cluster_addr(smem0, static_cast<uint32_t>(q));
+          float w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(w[i]) : "r"(base + at[i]));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = q ? v[i] + w[i] : w[i];
+        }
+      };
+      uint32_t at[4];
+      float v[4];
+      if (TRANS) {
+        const int row = threadIdx.x - 64;
+        for (int c0 = rank; c0 < cols; c0 += 4 * share) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) at[i] = static_cast<uint32_t>(min(c0 + i * share, BN - 1) * BM + row) * 4u;
+          add_up(at, v);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (c0 + i * share < cols && row < rows) out[(col0 + c0 + i * share) * p.ldo + row0 + row] = rounded<T>(v[i]);
+        }
+      } else {
+        constexpr int kPer = BN / 32, kRows = 4 / kPer;  // a row's accesses of a thread; rows at a time
+        for (int r0 = rank + share * (warp - 2); r0 < rows; r0 += 4 * kRows * share) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            at[i] = static_cast<uint32_t>(min(r0 + 4 * share * (i / kPer), BM - 1) * (BN + 1) + lane + 32 * (i % kPer)) * 4u;
+          add_up(at, v);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = r0 + 4 * share * (i / kPer), c = lane + 32 * (i % kPer);
+            if (r < rows && c < cols) out[(row0 + r) * p.ldo + col0 + c] = rounded<T>(v[i]);
+          }
+        }
+      }
+    }
+    cluster_sync();  // nobody leaves while its sums are read
+  } else {
+    __syncthreads();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -723,49 +793,57 @@ cudaError_t launch(const ProductParams& p, int sms, cudaStream_t s) {
   long long pairs = sms / 2;
   if (resident > 0 && pairs > resident) pairs = resident;
   if (pairs > tiles) pairs = tiles;
-  return launch_after(pair_kernel<T>, static_cast<int>(2 * pairs), kThreads, Cfg<T>::kSmem, s, p);
+  return launch_after(pair_kernel<T>, static_cast<int>(2 * pairs), kThreads, Cfg<T>::kSmem, s, 1, p);
 }
 
 }  // namespace pair
 
-template <int BN, typename T, bool TRANS>
+template <int BN, typename T, bool TRANS, bool SPLIT>
 cudaError_t launch_one(const ProductParams& p, int sms, cudaStream_t s) {
   static thread_local int configured_device = -1;
   int dev = 0;
   cudaGetDevice(&dev);
   if (configured_device != dev) {
-    cudaError_t e = cudaFuncSetAttribute(product_kernel<BN, T, TRANS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(product_kernel<BN, T, TRANS, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(Cfg<BN>::kSmem));
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
   const long long tiles = static_cast<long long>((p.m + BM - 1) / BM) * ((p.n + BN - 1) / BN);
-  return launch_after(product_kernel<BN, T, TRANS>, static_cast<int>(tiles < sms ? tiles : sms), kThreads, Cfg<BN>::kSmem, s, p);
+  const long long blocks = SPLIT ? tiles * p.split : tiles < sms ? tiles : sms;
+  return launch_after(product_kernel<BN, T, TRANS, SPLIT>, static_cast<int>(blocks), kThreads, Cfg<BN>::kSmem, s,
+                      SPLIT ? p.split : 1, p);
+}
+
+template <int BN, typename T, bool TRANS>
+cudaError_t launch_tiles(ProductParams p, int sms, cudaStream_t s) {
+  p.split = split_of(p.m, p.n, p.k, BN, sms);
+  return p.split > 1 ? launch_one<BN, T, TRANS, true>(p, sms, s) : launch_one<BN, T, TRANS, false>(p, sms, s);
 }
 
 template <typename T>
 cudaError_t launch_typed(const ProductParams& p, int sms, cudaStream_t s) {
   switch (product_tile_n(p.m, p.n, p.k, sms)) {
     case 256: return pair::launch<T>(p, sms, s);
-    case 32: return p.transposed ? launch_one<32, T, true>(p, sms, s) : launch_one<32, T, false>(p, sms, s);
-    case 64: return p.transposed ? launch_one<64, T, true>(p, sms, s) : launch_one<64, T, false>(p, sms, s);
-    default: return launch_one<128, T, false>(p, sms, s);
+    case 32: return p.transposed ? launch_tiles<32, T, true>(p, sms, s) : launch_tiles<32, T, false>(p, sms, s);
+    case 64: return p.transposed ? launch_tiles<64, T, true>(p, sms, s) : launch_tiles<64, T, false>(p, sms, s);
+    default: return launch_one<128, T, false, false>(p, sms, s);
   }
 }
 
 }  // namespace
 
 // 32 or 64 where the smaller side has so few rows.  Else 256 (pairs of CTAs) or
-// 128 (one CTA), whichever takes less time: measured, about 6.3 us + 0.35 us a
-// wave and stage along k for pairs, 4.2 us + 0.59 us for single CTAs (512 x 512 x
-// 1024: 7.7 against 6.5 us; x 8192: 17.5 against 22.9; 2048^3: 9.5 against 14.6).
+// 128 (one CTA), whichever takes less time: measured, about 6.0 us + 0.345 us a
+// wave and stage along k for pairs, 3.7 us + 0.46 us for single CTAs (512 x 512 x
+// 1024: 7.4 against 5.5 us; x 8192: 17.2 against 18.4; 2048^3: 9.4 against 12.0).
 int product_tile_n(int m, int n, int k, int sms) {
   if (n <= 64) return n <= 32 ? 32 : 64;
   auto waves = [](long long tiles, long long at_once) { return (tiles + at_once - 1) / at_once; };
   const long long pairs = waves(static_cast<long long>((m + 255) / 256) * ((n + 255) / 256), sms / 2);
   const long long single = waves(static_cast<long long>((m + 127) / 128) * ((n + 127) / 128), sms);
   const long long stages = (k + kStageK - 1) / kStageK;
-  return 210 + 35 * pairs * stages <= 59 * single * stages ? 256 : 128;
+  return 460 + 69 * pairs * stages <= 92 * single * stages ? 256 : 128;
 }
 
 cudaError_t launch_product(const ProductParams& p, int dtype, int sms, cudaStream_t s) {

@@ -362,7 +362,7 @@ cudaError_t quantize_as(const QuantParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
-  return launch_after(quantize_kernel<T, VEC, COLS>, p.ntiles, kThreads, smem, s, p);
+  return launch_after(quantize_kernel<T, VEC, COLS>, p.ntiles, kThreads, smem, s, 1, p);
 }
 
 // A launch reads eight values at once where all of its matrices allow it.
@@ -383,7 +383,7 @@ cudaError_t dequantize(const DequantParams& p, cudaStream_t s) {
   bool vec = true;
   for (int i = 0; i < p.nmat; ++i) vec = vec && p.mat[i].cols % 8 == 0 && reinterpret_cast<uintptr_t>(p.mat[i].y) % 16 == 0;
   if (vec) {
-    return launch_after(dequantize_kernel<T, true>, p.ntiles, kThreads, 0, s, p);
+    return launch_after(dequantize_kernel<T, true>, p.ntiles, kThreads, 0, s, 1, p);
   }
   constexpr int smem = kTile * kTile * static_cast<int>(sizeof(T));
   static thread_local int configured_device = -1;
@@ -394,7 +394,7 @@ cudaError_t dequantize(const DequantParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
-  return launch_after(dequantize_kernel<T, false>, p.ntiles, kThreads, smem, s, p);
+  return launch_after(dequantize_kernel<T, false>, p.ntiles, kThreads, smem, s, 1, p);
 }
 
 }  // namespace

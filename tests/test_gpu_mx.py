@@ -186,7 +186,7 @@ PRODUCTS = [(1, 1, 1), (1, 128, 32), (1, 130, 777), (3, 500, 96), (17, 300, 256)
             (64, 1000, 128), (65, 64, 96), (100, 7, 513), (128, 128, 128), (129, 257, 288), (300, 200, 1000),
             (512, 384, 2048), (1000, 777, 333), (257, 1500, 64), (700, 33, 4000), (2000, 1900, 256)]
 # tiles of 256 x 256: several a pair of CTAs, every remainder of k within a stage, ragged edges
-PRODUCTS += [(4100, 4200, k) for k in (32, 40, 96, 130, 192, 224, 256)] + [(2100, 2301, 300), (2100, 2300, 1111), (256, 300, 5000), (5000, 1025, 96)]
+PRODUCTS += [(4100, 4200, k) for k in (32, 40, 96, 130, 192, 224, 256)] + [(4100, 4201, 300), (2100, 2300, 1111), (16, 4096, 4096), (40, 300, 5000), (300, 20, 3000), (130, 50, 700), (256, 300, 5000), (5000, 1025, 96)]
 
 
 @pytest.mark.parametrize("m,n,k", PRODUCTS)
@@ -199,7 +199,7 @@ def test_product(m, n, k):
     assert nsb.muon_get_status() == 0
 
 
-@pytest.mark.parametrize("m,n", [(200, 150), (20, 300), (300, 60), (2100, 2300)])
+@pytest.mark.parametrize("m,n", [(200, 150), (20, 300), (300, 60), (4100, 4200)])
 def test_product_scales_far_apart(m, n):
     """Each block its own scale, over many powers of two: every scale byte reaches its own block."""
     g = torch.Generator().manual_seed(9)
