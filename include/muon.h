@@ -429,9 +429,9 @@ int muon_mx_dequantize(int count, const void* const* data, const void* const* sc
  *   y  = A = rows of x,    B = rows of W
  *   dx = A = rows of dy,   B = columns of W
  *   dW = A = columns of dy, B = columns of x
- * A wait that runs out is recorded as for the other tensor-core calls; of a
- * captured call on a stream that had no status word, in one word a device,
- * which muon_get_status of any stream of it reports.
+ * A wait that runs out is recorded as for the other tensor-core calls; in a
+ * captured call, in one word a device, which muon_get_status of any stream of
+ * it reports.
  */
 int muon_mx_product(long long m, long long n, long long k, const void* a_data, const void* a_scales, const void* b_data,
                     const void* b_scales, void* out, long long ldo, int dtype, void* stream);

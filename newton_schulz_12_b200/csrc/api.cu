@@ -80,7 +80,7 @@ std::map<std::pair<int, uintptr_t>, Workspace> g_ws;
 std::map<int, DevInfo> g_dev;
 unsigned long long g_timeout_ns = 2000000000ull;
 int g_inject = 0;
-std::atomic<bool> g_captured_launches{false};  // a captured launch without a status word of its stream
+std::atomic<bool> g_captured_launches{false};  // there was a captured launch of muon_mx_product
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -1295,19 +1295,9 @@ int device_sms(int* sms) {
   return MUON_OK;
 }
 
-// A stream under capture that has no status word yet gets none (allocating
-// one would end the capture): null, and the kernel takes its own.
+// A captured launch gets none: allocating one would end the capture, and the
+// graph may outlive the stream's (muon_release).  The kernel takes its own then.
 int workspace_status(cudaStream_t s, int** status) {
-  int dev = 0;
-  CUDA_TRY(cudaGetDevice(&dev));
-  {
-    std::lock_guard<std::mutex> lk(g_mu);
-    auto it = g_ws.find({dev, reinterpret_cast<uintptr_t>(s)});
-    if (it != g_ws.end() && it->second.status) {
-      *status = it->second.status;
-      return MUON_OK;
-    }
-  }
   cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
   if (cudaStreamIsCapturing(s, &capture) != cudaSuccess) {
     cudaGetLastError();  // the legacy stream while another one captures

@@ -1,6 +1,6 @@
 // C ABI of the operators around a Muon-trained linear layer: layer norm with
 // its gradient, and 4-bit microscaled quantisation and products.  Arguments
-// are checked on the host before anything is enqueued; no call allocates.
+// are checked on the host before anything is enqueued; no call takes a workspace.
 #include <cmath>
 #include <new>
 

@@ -450,7 +450,7 @@ struct ProductParams {
 // has as many rows, or half as many for tiles of 256 (a pair of CTAs).
 int product_tile_n(int m, int n, int k, int sms);
 cudaError_t launch_product(const ProductParams& p, int dtype, int sms, cudaStream_t s);
-// Reads and clears the current device's status word of captured launches.
+// Reads and clears the current device's status word of captured products.
 cudaError_t take_captured_status(int* value);
 
 }  // namespace mx
@@ -485,7 +485,7 @@ namespace host {
 int set_error(int code, const char* fmt, ...);
 void clear_error();
 int device_sms(int* sms);                       // checks the device, too
-int workspace_status(cudaStream_t s, int** status);  // device status word of (current device, stream)
+int workspace_status(cudaStream_t s, int** status);  // status word of (current device, stream), null under capture
 unsigned long long wait_timeout_ns();
 int take_injection();                           // the pending fault-injection mode, which it clears
 // A 2-D map of bytes with 128-byte swizzle (`words` false) or of 4-byte words without.

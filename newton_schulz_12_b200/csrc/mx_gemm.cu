@@ -26,8 +26,7 @@ constexpr int kStageK = 256;           // values of k a stage: 128 bytes of data
 constexpr int kThreads = 192;          // copier, issuer, four epilogue warps
 constexpr int kScaleTile = 512;        // bytes: 128 rows x 4 blocks
 
-// Where a wait that runs out in a captured launch is recorded when the stream
-// had no status word at capture (see workspace_status).
+// Where a wait that runs out in a captured launch is recorded (see workspace_status).
 __device__ int g_captured_status;
 
 template <int BN>

@@ -261,6 +261,29 @@ def test_a_wait_that_runs_out_is_reported(m, n, k):
     assert nsb.muon_get_status() == 0
 
 
+def test_a_wait_that_runs_out_in_a_graph_is_reported():
+    """The graph outlives the stream's own status word; any stream reports it, once."""
+    a, b = nsb.muon_mx_quantize([torch.randn(300, 600).cuda(), torch.randn(200, 600).cuda()])
+    want = nsb.muon_mx_product(a, b)
+    torch.cuda.synchronize()
+    nsb.muon_set_wait_timeout_ms(200)
+    graph = torch.cuda.CUDAGraph()
+    try:
+        nsb.muon_set_fault_injection(1)
+        with torch.cuda.graph(graph, stream=streams()[1]):
+            nsb.muon_mx_product(a, b)
+    finally:
+        nsb.muon_set_fault_injection(0)
+        nsb.muon_set_wait_timeout_ms(2000)
+    nsb.muon_release()
+    assert nsb.muon_get_status() == 0
+    graph.replay()
+    assert nsb.muon_get_status() == -5
+    assert nsb.muon_get_status(streams()[1]) == 0 and nsb.muon_get_status() == 0
+    assert torch.equal(nsb.muon_mx_product(a, b), want)
+    assert nsb.muon_get_status() == 0
+
+
 def test_kernels_are_timed():
     x, dy, w, b, W = make(64, 128, 256)
     Wr, Wc = nsb.muon_mx_quantize(W, rows=True, cols=True)
