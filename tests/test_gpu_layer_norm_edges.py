@@ -1,0 +1,25 @@
+"""Rows of layer norm at the ends of what its types hold, against what the formulas give there."""
+import pytest
+import torch
+
+import newton_schulz_12_b200 as nsb
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+@pytest.mark.parametrize("rows", [5, 9601])
+@pytest.mark.parametrize("cols", [256, 896, 1792, 3584, 1021])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_constant_rows(rows, cols, dtype):
+    """A row of one value whose sums are exact in fp32 has that mean: y is the bias, and dx of one dy is 0.
+
+    1000 * cols and all partial sums are multiples of 1000 below 1000 * 2^24 / 1000, so exact; so are
+    multiples of 0.5."""
+    x = torch.full((rows, cols), 1000.0, dtype=dtype, device="cuda")
+    y, mean, rstd = nsb.muon_layer_norm(x)
+    assert (mean == 1000).all() and (y == 0).all()
+    assert ((rstd.double() * 1e-5 ** 0.5 - 1).abs() <= 4 * U + 1e-7).all()
+    dx, _, _ = nsb.muon_layer_norm_backward(torch.full_like(x, 0.5), x, mean, rstd)
+    assert (dx == 0).all()
