@@ -257,9 +257,10 @@ __device__ __forceinline__ void narrow<__half>(f32x2 v, __half* out) {
 }
 
 // 1 / sqrt(v): the hardware's estimate (2 fp32 units) and one Newton step, left
-// out where it would make a NaN of 0 or an infinity.
+// out where it would make a NaN of 0 or an infinity.  v y comes first: half of
+// v itself would round where v is subnormal.
 __device__ __forceinline__ float reciprocal_root(float v) {
-  const float y = rsqrtf(v), z = y * fmaf(-0.5f * v * y, y, 1.5f);
+  const float y = rsqrtf(v), z = y * fmaf(v * y, -0.5f * y, 1.5f);
   return v > 0.f && y > 0.f ? z : y;
 }
 

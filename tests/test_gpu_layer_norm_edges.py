@@ -23,3 +23,18 @@ def test_constant_rows(rows, cols, dtype):
     assert ((rstd.double() * 1e-5 ** 0.5 - 1).abs() <= 4 * U + 1e-7).all()
     dx, _, _ = nsb.muon_layer_norm_backward(torch.full_like(x, 0.5), x, mean, rstd)
     assert (dx == 0).all()
+
+
+@pytest.mark.parametrize("cols", [4, 32, 1024])
+@pytest.mark.parametrize("power", [-74, -70, -62, 0, 40, 58])
+def test_variance_at_the_ends_of_fp32(cols, power):
+    """A row of +-2^power in half of its places (a quarter each), no eps: every sum is exact, the variance is
+    2^(2 power - 1), down to the smallest number there is."""
+    q = cols // 4
+    x = torch.zeros(3, cols, device="cuda")
+    x[:, :q], x[:, q:2 * q] = 2.0 ** power, -2.0 ** power
+    y, mean, rstd = nsb.muon_layer_norm(x, eps=0.0)
+    want = 2.0 ** (0.5 - power)
+    assert (mean == 0).all()
+    assert ((rstd.double() / want - 1).abs() <= 4 * U).all()
+    assert ((y.double() - x.double() * want).abs() <= 5 * U * 2 ** 0.5).all()
