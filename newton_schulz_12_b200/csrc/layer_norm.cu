@@ -610,7 +610,9 @@ __global__ void __launch_bounds__(kFwdThreads) forward_kernel(const FwdParams p,
 // SUMS: each thread also adds up its columns' dy xhat and dy over the rows of
 // its group; the block's groups are added in their order at the end and the
 // block writes one partial.  Values beyond the row are zeros of dy, so they
-// add nothing; rows beyond the matrix have rstd 0.
+// add nothing (where mean * rstd is beyond fp32, x = 0 there would make xhat
+// infinite, and 0 times that a NaN: they take the mean then); rows beyond the
+// matrix have rstd 0.
 template <typename T, typename P, int VEC, int NV, int R, bool SUMS, bool RING>
 __global__ void __launch_bounds__(SUMS ? kBwdThreads : kFwdThreads) backward_kernel(const BwdParams p, int tpr, int groups, int depth) {
   previous_kernel_done();
@@ -695,6 +697,20 @@ __global__ void __launch_bounds__(SUMS ? kBwdThreads : kFwdThreads) backward_ker
       }
     }
     if (RING && ++slot == depth) slot = 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      float m, r1;
+      f2_split(mean[i], m, r1);
+      f2_split(rr[i], r1, r1);
+      if (!(fabsf(m * r1) < __int_as_float(0x7F800000))) {  // hardly ever: beyond the row the mean, whose xhat is 0
+#pragma unroll
+        for (int k = 0; k < E / 2; ++k) {
+          float lo, hi;
+          f2_split(xhat[i][k], lo, hi);
+          xhat[i][k] = f2((VEC > 1 ? 2 * k / VEC : 2 * k) < nv ? lo : m, (VEC > 1 ? 2 * k / VEC : 2 * k + 1) < nv ? hi : m);
+        }
+      }
+    }
     f32x2 a[R], c[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) a[i] = c[i] = f2(0.f, 0.f);

@@ -38,3 +38,22 @@ def test_variance_at_the_ends_of_fp32(cols, power):
     assert (mean == 0).all()
     assert ((rstd.double() / want - 1).abs() <= 4 * U).all()
     assert ((y.double() - x.double() * want).abs() <= 5 * U * 2 ** 0.5).all()
+
+
+@pytest.mark.parametrize("rows", [3, 40000])
+@pytest.mark.parametrize("cols", [5, 40])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_gradient_of_constant_rows_far_from_zero(rows, cols, dtype):
+    """Equal values of 2^120 in a row: mean * rstd has no fp32 number, but no value of the formula needs it.
+
+    The sums are exact (40 * 2^120 is below 2^126), xhat is 0, so dx = rstd (dy - mean(dy))."""
+    x = torch.full((rows, cols), 2.0 ** 120, dtype=dtype, device="cuda")
+    dy = torch.arange(1, cols + 1, device="cuda").to(dtype).repeat(rows, 1)
+    y, mean, rstd = nsb.muon_layer_norm(x)
+    assert (mean == 2.0 ** 120).all() and (y == 0).all()
+    dx, _, db = nsb.muon_layer_norm_backward(dy, x, mean, rstd, bias=True)
+    R = rstd.double()[:, None]
+    want = (dy.double() - (cols + 1) / 2) * R
+    half = torch.finfo(dtype).eps / 2
+    assert ((dx.double() - want).abs() <= (half + 4 * U) * want.abs() + 4 * U * cols * R).all()
+    assert (db.double() == dy.double().sum(0)).all()
