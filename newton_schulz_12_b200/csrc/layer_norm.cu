@@ -861,16 +861,21 @@ cudaError_t forward_with(const FwdParams& p, const Shape& h, int sms, cudaStream
 bool many_rows(long long rows, const Shape& h, int sms) { return rows >= 4ll * sms * h.groups; }
 
 // Two rows a group at once where the registers and two slots allow it (8192 x
-// 8192 bf16, 32 values a thread: 57.8 us against 71.6 with one).
+// 8192 bf16, 32 values a thread: 57.8 us against 71.6 with one).  Rows of up to
+// 24 values a thread have 96 threads at most: their slots always fit.
 template <typename T, typename P, int VEC, int NV>
 cudaError_t forward_as(const FwdParams& p, const Shape& h, int sms, cudaStream_t s) {
-  constexpr bool kTwo = VEC > 1 && (VEC * NV <= 24 || sizeof(T) == 2);
   if constexpr (VEC > 1 || sizeof(T) == 4) {
     if (many_rows(p.rows, h, sms)) {
-      const int slot = h.tpr * h.groups * Ring<T, VEC, NV>::kRow, params = 2 * VEC * NV * h.tpr * 4;
-      if constexpr (kTwo)
-        if (4 * slot + params <= kSmemBudget) return forward_with<T, P, VEC, NV, 2, true>(p, h, sms, s);
-      return forward_with<T, P, VEC, NV, 1, true>(p, h, sms, s);
+      if constexpr (VEC > 1 && VEC * NV <= 24) {
+        return forward_with<T, P, VEC, NV, 2, true>(p, h, sms, s);
+      } else {
+        if constexpr (VEC > 1 && sizeof(T) == 2) {
+          const int slot = h.tpr * h.groups * Ring<T, VEC, NV>::kRow, params = 2 * VEC * NV * h.tpr * 4;
+          if (4 * slot + params <= kSmemBudget) return forward_with<T, P, VEC, NV, 2, true>(p, h, sms, s);
+        }
+        return forward_with<T, P, VEC, NV, 1, true>(p, h, sms, s);
+      }
     }
   }
   return forward_with<T, P, VEC, NV, 1, false>(p, h, sms, s);
@@ -954,9 +959,7 @@ cudaError_t backward(BwdParams p, int sms, cudaStream_t s) {
       e = vec ? backward_as<T, P, V, 16 / V, true>(p, h, sms, s) : backward_as<T, P, 1, 16, true>(p, h, sms, s);
     else if (held)
       e = vec ? backward_as<T, P, V, 24 / V, true>(p, h, sms, s) : backward_as<T, P, 1, 24, true>(p, h, sms, s);
-    else if (h.e == 24)  // 9217 .. 12288 columns
-      e = vec ? backward_as<T, P, V, 24 / V, false>(p, h, sms, s) : backward_as<T, P, 1, 24, false>(p, h, sms, s);
-    else if (h.e == 32)
+    else if (h.e == 32)  // 9217 .. 16384 columns
       e = vec ? backward_as<T, P, V, 32 / V, false>(p, h, sms, s) : backward_as<T, P, 1, 32, false>(p, h, sms, s);
     else {
       const long long want = static_cast<long long>(sms) * 4;
