@@ -222,6 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   uint64_t* bars = reinterpret_cast<uint64_t*>(staging + 4 * C::kStagingWarp);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  volatile int* stages_copied = abort_flag + 1;  // started, by the end of the copier's loop
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t bar0 = smem_u32(bars), smem0 = smem_u32(smem);
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
@@ -270,8 +271,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 
   if (warp == 0) {
     if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, issued = 0, parity = 0;
+      int stage = 0, copied = 0;
+      uint32_t phase = 0;
       bool ok = true, withhold = p.inject == 1 && blockIdx.x == 0;
       for (int t = first; t < tiles && ok; t += stride) {
         const int tm = t % tiles_m, tn = t / tiles_m;
@@ -284,8 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           }
           const uint32_t sbytes = static_cast<uint32_t>(min(2, ktiles - 2 * it)) * kScaleTile;  // this stage's, along k
           mbar_arrive_expect_tx(full_bar(stage), C::kABytes + C::kBBytes + 2 * sbytes);
-          issued |= 1u << stage;
-          parity = (parity & ~(1u << stage)) | (phase << stage);
+          ++copied;
           const uint32_t a = smem0 + stage * C::kStageBytes, b = a + C::kABytes, sa = b + C::kBBytes, sb = sa + C::kScaleA;
           if (!withhold) tma_load_2d(a, &p.a, full_bar(stage), it * 128, tm * BM);
           withhold = false;
@@ -298,9 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           }
         }
       }
-      if (!ok)
-        for (int s = 0; s < S; ++s)
-          if (issued & (1u << s)) mbar_wait_drain(full_bar(s), (parity >> s) & 1u, drain_ns);
+      *stages_copied = copied;
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -475,6 +473,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   } else {
     __syncthreads();
   }
+  // A wait ran out: the last stages may still be landing, also where their copier
+  // had finished.
+  if (threadIdx.x == 0 && *abort_flag) {
+    const int copied = *stages_copied;
+    for (int i = max(0, copied - S); i < copied; ++i) mbar_wait_drain(full_bar(i % S), (i / S) & 1, drain_ns);
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -537,6 +541,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(staging + kEpiWarps * 32 * C::kRow);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  volatile int* stages_copied = abort_flag + 1;  // started, by the end of this CTA's copier's loop
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
   const uint32_t peer = static_cast<uint32_t>(rank ^ 1);
@@ -593,8 +598,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // copies, in both CTAs
     if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, issued = 0, parity = 0;
+      int stage = 0, copied = 0;
+      uint32_t phase = 0;
       bool ok = true, withhold = p.inject == 1 && blockIdx.x == 0;
       for (int t = first; t < tiles && ok; t += npairs) {
         int tm, tn;
@@ -608,8 +613,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           // what lies beyond a matrix comes as zeros and counts
           if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2 * (kABytes + kBBytes));
           mbar_arrive_expect_tx(landed_bar(stage), kScaleA + kScaleB);
-          issued |= 1u << stage;
-          parity = (parity & ~(1u << stage)) | (phase << stage);
+          ++copied;
           const uint32_t a = smem0 + stage * kStageBytes, b = a + kABytes, sa = b + kBBytes, sb = sa + kScaleA;
           tma_load_2d(sa, &p.sa, landed_bar(stage), it * 256, 2 * tm + rank);
           tma_load_2d(sb, &p.sb, landed_bar(stage), it * 256, 2 * tn);
@@ -622,12 +626,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (!ok)
-        for (int s = 0; s < S; ++s)
-          if (issued & (1u << s)) {
-            if (rank == 0) mbar_wait_drain(full_bar(s), (parity >> s) & 1u, drain_ns);
-            mbar_wait_drain(landed_bar(s), (parity >> s) & 1u, drain_ns);
-          }
+      *stages_copied = copied;
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -765,6 +764,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   cluster_sync();
+  if (*abort_flag) {  // in both CTAs or in neither (whoever gives up sets both)
+    // A wait ran out: the last stages may still be landing, also where their
+    // copier had finished.  The leader's barriers count the operands of both;
+    // stages that only the partner has started are armed for its half now.
+    if (threadIdx.x == 0) {
+      const int copied = *stages_copied;
+      for (int i = max(0, copied - S); i < copied; ++i) {
+        if (rank == 0) mbar_wait_drain(full_bar(i % S), (i / S) & 1, drain_ns);
+        mbar_wait_drain(landed_bar(i % S), (i / S) & 1, drain_ns);
+      }
+      if (rank == 0) {
+        int theirs;
+        asm volatile("ld.shared::cluster.s32 %0, [%1];"
+                     : "=r"(theirs)
+                     : "r"(cluster_addr(smem_u32(const_cast<int*>(stages_copied)), 1)));
+        for (int i = copied; i < theirs; ++i) {
+          mbar_arrive_expect_tx(full_bar(i % S), kABytes + kBBytes);
+          mbar_wait_drain(full_bar(i % S), (i / S) & 1, drain_ns);
+        }
+      }
+    }
+    __syncwarp();
+    cluster_sync();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
