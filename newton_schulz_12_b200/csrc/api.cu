@@ -1308,9 +1308,24 @@ int workspace_status(cudaStream_t s, int** status) {
     *status = nullptr;
     return MUON_OK;
   }
-  Workspace* ws = nullptr;
-  MUON_TRY(get_workspace(s, 0, &ws));
-  *status = ws->status;
+  int dev = 0;
+  CUDA_TRY(cudaGetDevice(&dev));
+  std::lock_guard<std::mutex> lk(g_mu);
+  Workspace& w = g_ws[{dev, reinterpret_cast<uintptr_t>(s)}];
+  if (!w.status) {
+    // another stream may be capturing: the allocation must not end that, and
+    // the word is cleared on this stream
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    CUDA_TRY(cudaThreadExchangeStreamCaptureMode(&mode));
+    int* word = nullptr;
+    cudaError_t e = cudaMalloc(&word, 256);
+    if (e == cudaSuccess) e = cudaMemsetAsync(word, 0, 256, s);
+    if (e != cudaSuccess && word) cudaFree(word);
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess) return set_err(MUON_ERR_ALLOC, "status word: %s", cudaGetErrorString(e));
+    w.status = word;
+  }
+  *status = w.status;
   return MUON_OK;
 }
 

@@ -1,6 +1,7 @@
 // C ABI of the operators around a Muon-trained linear layer: layer norm with
 // its gradient, and 4-bit microscaled quantisation and products.  Arguments
-// are checked on the host before anything is enqueued; no call takes a workspace.
+// are checked on the host before anything is enqueued; no call takes a workspace
+// (a product has its stream's status word, which the first one allocates).
 #include <cmath>
 #include <new>
 
