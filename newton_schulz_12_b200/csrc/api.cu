@@ -1675,7 +1675,7 @@ int muon_get_status(void* stream) {
   CUDA_TRY(cudaGetDevice(&dev));
   if (g_captured_launches) {
     int captured = 0;
-    CUDA_TRY(mx::take_captured_status(&captured));
+    CUDA_TRY(mx::take_captured_status(s, &captured));
     if (captured != 0)
       return set_err(captured, "device status %d (a bounded device-side wait ran out in a captured launch)", captured);
   }

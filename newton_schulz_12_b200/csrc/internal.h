@@ -450,8 +450,8 @@ struct ProductParams {
 // has as many rows, or half as many for tiles of 256 (a pair of CTAs).
 int product_tile_n(int m, int n, int k, int sms);
 cudaError_t launch_product(const ProductParams& p, int dtype, int sms, cudaStream_t s);
-// Reads and clears the current device's status word of captured products.
-cudaError_t take_captured_status(int* value);
+// Reads and clears the current device's status word of captured products, on `s`, and waits for it.
+cudaError_t take_captured_status(cudaStream_t s, int* value);
 
 }  // namespace mx
 

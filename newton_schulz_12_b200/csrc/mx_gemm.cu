@@ -16,6 +16,8 @@
 
 #include <cuda_fp16.h>
 
+#include <mutex>
+
 namespace muon {
 namespace mx {
 
@@ -28,6 +30,8 @@ constexpr int kScaleTile = 512;        // bytes: 128 rows x 4 blocks
 
 // Where a wait that runs out in a captured launch is recorded (see workspace_status).
 __device__ int g_captured_status;
+__device__ int g_taken_status;  // take_captured_status: what it held
+__global__ void take_status_kernel() { g_taken_status = atomicExch(&g_captured_status, 0); }
 
 template <int BN>
 struct Cfg {
@@ -872,11 +876,15 @@ cudaError_t launch_product(const ProductParams& p, int dtype, int sms, cudaStrea
   return dtype == 1 ? launch_typed<float>(p, sms, s) : dtype == 0 ? launch_typed<bf16>(p, sms, s) : launch_typed<__half>(p, sms, s);
 }
 
-cudaError_t take_captured_status(int* value) {
-  cudaError_t e = cudaMemcpyFromSymbol(value, g_captured_status, sizeof(int));
-  if (e != cudaSuccess || *value == 0) return e;
-  const int zero = 0;
-  return cudaMemcpyToSymbol(g_captured_status, &zero, sizeof(int));
+// The word is taken in one step on the device, so that a wait that runs out
+// meanwhile (a graph on another stream) is not lost.
+cudaError_t take_captured_status(cudaStream_t s, int* value) {
+  static std::mutex mu;  // one g_taken_status a device
+  std::lock_guard<std::mutex> lk(mu);
+  take_status_kernel<<<1, 1, 0, s>>>();
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbolAsync(value, g_taken_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+  return e == cudaSuccess ? cudaStreamSynchronize(s) : e;
 }
 
 }  // namespace mx

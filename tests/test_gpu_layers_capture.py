@@ -54,3 +54,34 @@ def test_memory_of_the_layer_operators():
     s.synchronize()
     nsb.muon_release()
     assert held(s) == 0
+
+
+def test_a_captured_wait_that_runs_out_is_reported_once_whoever_asks_meanwhile():
+    g = torch.Generator().manual_seed(1)
+    a, b = nsb.muon_mx_quantize([torch.randn(300, 200, generator=g).cuda(), torch.randn(200, 200, generator=g).cuda()])
+    want = nsb.muon_mx_product(a, b)
+    s, asking = torch.cuda.Stream(), torch.cuda.Stream()
+    graphs = []
+    nsb.muon_set_wait_timeout_ms(50)
+    try:
+        for _ in range(2):
+            nsb.muon_set_fault_injection(1)
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[-1], stream=s):
+                nsb.muon_mx_product(a, b)
+    finally:
+        nsb.muon_set_fault_injection(0)
+        nsb.muon_set_wait_timeout_ms(2000)
+    assert nsb.muon_get_status(asking) == 0
+    for graph in graphs:
+        reports = 0
+        with torch.cuda.stream(s):
+            graph.replay()
+            done = torch.cuda.Event()
+            done.record()
+        while not done.query():
+            reports += nsb.muon_get_status(asking) == -5
+        reports += nsb.muon_get_status(asking) == -5
+        assert reports == 1
+        assert nsb.muon_get_status(s) == 0
+    assert torch.equal(nsb.muon_mx_product(a, b), want)
