@@ -337,8 +337,10 @@ int muon_bx_apply_bf16(int batch, int m, int n, int ldx, const void* B, int ldb,
  * They follow the conventions above, except that their matrices may have a row
  * stride (ld, in elements, >= cols; not looked at for one row), need only the
  * alignment of their element type, and may have up to 2^30 rows and columns,
- * zero rows among them.  An output matrix must not overlap an input, counted
- * from its first to its last element (MUON_ERR_ARG).  They take no workspace
+ * zero rows among them.  What a call writes (matrices, vectors, scales, scratch)
+ * must not overlap anything else that it reads or writes, a matrix counted from
+ * its first to its last element (MUON_ERR_ARG); a list's matrices count as one
+ * call.  They take no workspace
  * but, for products, the stream's status word (256 bytes, allocated by the
  * first one and freed by muon_release; no other stream's capture is disturbed),
  * and can be captured into a CUDA graph from their first call on a stream;

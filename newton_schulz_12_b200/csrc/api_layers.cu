@@ -2,8 +2,11 @@
 // its gradient, and 4-bit microscaled quantisation and products.  Arguments
 // are checked on the host before anything is enqueued; no call takes a workspace
 // (a product has its stream's status word, which the first one allocates).
+#include <algorithm>
 #include <cmath>
+#include <iterator>
 #include <new>
+#include <vector>
 
 #include "internal.h"
 #include "muon.h"
@@ -57,10 +60,42 @@ int check_stride(long long rows, long long cols, long long ld, const char* what)
 
 long long extent(long long rows, long long cols, long long ld) { return rows ? (rows - 1) * ld + cols : 0; }
 
-// Whether two matrices share bytes of their extents.
-bool overlap(const void* a, long long abytes, const void* b, long long bbytes) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && abytes > 0 && bbytes > 0 && x < y + static_cast<uintptr_t>(bbytes) && y < x + static_cast<uintptr_t>(abytes);
+// Memory that a call reads or writes: a matrix from its first to its last element.
+struct Span {
+  uintptr_t at, end;
+  bool out;
+  const char* what;
+};
+
+Span reads(const void* p, long long bytes, const char* what) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  return {at, p && bytes > 0 ? at + static_cast<uintptr_t>(bytes) : at, false, what};
+}
+
+Span writes(const void* p, long long bytes, const char* what) {
+  Span s = reads(p, bytes, what);
+  s.out = true;
+  return s;
+}
+
+// What is written shares no byte with anything else of the call.
+int check_apart(Span* spans, size_t count) {
+  std::sort(spans, spans + count, [](const Span& a, const Span& b) { return a.at < b.at; });
+  const Span *any = nullptr, *out = nullptr;  // those that reach farthest so far, of all and of the written ones
+  for (size_t i = 0; i < count; ++i) {
+    const Span& s = spans[i];
+    if (s.end == s.at) continue;
+    const Span* other = s.out ? any : out;
+    if (other && other->end > s.at)
+      return host::set_error(MUON_ERR_ARG, "%s must not overlap %s", s.out ? s.what : other->what, s.out ? other->what : s.what);
+    if (!any || s.end > any->end) any = &s;
+    if (s.out && (!out || s.end > out->end)) out = &s;
+  }
+  return MUON_OK;
+}
+
+long long scale_bytes(long long rows, long long cols) {
+  return ((rows + mx::kTile - 1) / mx::kTile) * ((cols + mx::kTile - 1) / mx::kTile) * 512;
 }
 
 int check_params(const void* weight, const void* bias, int dtype, int param_dtype) {
@@ -89,9 +124,10 @@ int forward_impl(long long rows, long long cols, const void* x, long long ldx, i
   TRY(check_pointer(y, e, "y"));
   TRY(check_pointer(mean, 4, "mean"));
   TRY(check_pointer(rstd, 4, "rstd"));
-  const long long pe = element_size(param_dtype) * cols, yb = extent(rows, cols, ldy) * e;
-  if (overlap(y, yb, x, extent(rows, cols, ldx) * e) || overlap(y, yb, weight, pe) || overlap(y, yb, bias, pe))
-    return host::set_error(MUON_ERR_ARG, "y must not overlap x, weight or bias");
+  const long long pe = element_size(param_dtype) * cols;
+  Span spans[] = {writes(y, extent(rows, cols, ldy) * e, "y"), writes(mean, rows * 4, "mean"), writes(rstd, rows * 4, "rstd"),
+                  reads(x, extent(rows, cols, ldx) * e, "x"),  reads(weight, pe, "weight"),    reads(bias, pe, "bias")};
+  TRY(check_apart(spans, std::size(spans)));
   int sms = 0;
   TRY(host::device_sms(&sms));
   ln::FwdParams p{};
@@ -133,11 +169,13 @@ int backward_impl(long long rows, long long cols, const void* dy, long long lddy
     TRY(check_pointer(mean, 4, "mean"));
     TRY(check_pointer(rstd, 4, "rstd"));
     TRY(check_pointer(dx, e, "dx"));
-    const long long db = extent(rows, cols, lddx) * e;
-    if (overlap(dx, db, x, extent(rows, cols, ldx) * e) || overlap(dx, db, dy, extent(rows, cols, lddy) * e) ||
-        overlap(dx, db, weight, cols * element_size(param_dtype)))
-      return host::set_error(MUON_ERR_ARG, "dx must not overlap dy, x or weight");
   }
+  const long long pe = element_size(param_dtype) * cols;
+  Span spans[9] = {writes(dx, extent(rows, cols, lddx) * e, "dx"), writes(dweight, pe, "dweight"),
+                   writes(dbias, pe, "dbias"),                    reads(dy, extent(rows, cols, lddy) * e, "dy"),
+                   reads(x, extent(rows, cols, ldx) * e, "x"),    reads(weight, pe, "weight"),
+                   reads(mean, rows * 4, "mean"),                 reads(rstd, rows * 4, "rstd")};
+  TRY(check_apart(spans, 8));
   if (rows == 0 && !dweight && !dbias) return MUON_OK;
   int sms = 0;
   TRY(host::device_sms(&sms));
@@ -147,6 +185,8 @@ int backward_impl(long long rows, long long cols, const void* dy, long long lddy
     if (scratch_bytes < need)
       return host::set_error(MUON_ERR_ARG, "scratch of %lld bytes: %lld are needed (muon_layer_norm_scratch_bytes)", scratch_bytes, need);
     TRY(check_pointer(scratch, 16, "scratch"));
+    spans[8] = writes(scratch, need, "scratch");
+    TRY(check_apart(spans, 9));
   }
   ln::BwdParams p{};
   p.rows = rows;
@@ -189,6 +229,8 @@ int quantize_impl(int count, const void* const* x, const int64_t* shapes, const 
   if (count == 0) return MUON_OK;
   if (!x || !shapes) return host::set_error(MUON_ERR_ARG, "x and shapes must be non-NULL");
   const long long e = element_size(dtype);
+  std::vector<Span> spans;  // all matrices' together: they may be written at the same time
+  spans.reserve(static_cast<size_t>(count) * 5);
   for (int i = 0; i < count; ++i) {
     TRY(check_matrix(shapes, i));
     const long long r = shapes[2 * i], c = shapes[2 * i + 1];
@@ -201,11 +243,17 @@ int quantize_impl(int count, const void* const* x, const int64_t* shapes, const 
     if (col_data) TRY(check_pointer(col_scales[i], 16, "col_scales"));
     if (static_cast<long long>(tile_count(r)) * tile_count(c) >= (1ll << 31))
       return host::set_error(MUON_ERR_SHAPE, "matrix %d: %lld x %lld has too many tiles", i, r, c);
-    const long long xb = extent(r, c, strides ? strides[i] : c) * e;
-    if ((row_data && overlap(x[i], xb, row_data[i], r * mx::data_stride(c))) ||
-        (col_data && overlap(x[i], xb, col_data[i], c * mx::data_stride(r))))
-      return host::set_error(MUON_ERR_ARG, "matrix %d: its forms must not overlap it", i);
+    spans.push_back(reads(x[i], extent(r, c, strides ? strides[i] : c) * e, "x"));
+    if (row_data) {
+      spans.push_back(writes(row_data[i], r * mx::data_stride(c), "row_data"));
+      spans.push_back(writes(row_scales[i], scale_bytes(r, c), "row_scales"));
+    }
+    if (col_data) {
+      spans.push_back(writes(col_data[i], c * mx::data_stride(r), "col_data"));
+      spans.push_back(writes(col_scales[i], scale_bytes(r, c), "col_scales"));
+    }
   }
+  TRY(check_apart(spans.data(), spans.size()));
   int sms = 0;
   TRY(host::device_sms(&sms));
   cudaStream_t s = as_stream(stream);
@@ -245,6 +293,8 @@ int dequantize_impl(int count, const void* const* data, const void* const* scale
   TRY(check_dtype(dtype));
   if (count == 0) return MUON_OK;
   if (!data || !scales || !shapes || !y) return host::set_error(MUON_ERR_ARG, "data, scales, shapes and y must be non-NULL");
+  std::vector<Span> spans;
+  spans.reserve(static_cast<size_t>(count) * 3);
   for (int i = 0; i < count; ++i) {
     TRY(check_matrix(shapes, i));
     const long long r = shapes[2 * i], c = shapes[2 * i + 1];
@@ -254,9 +304,11 @@ int dequantize_impl(int count, const void* const* data, const void* const* scale
     TRY(check_pointer(y[i], element_size(dtype), "y"));
     if (static_cast<long long>(tile_count(r)) * tile_count(c) >= (1ll << 31))
       return host::set_error(MUON_ERR_SHAPE, "matrix %d: %lld x %lld has too many tiles", i, r, c);
-    if (overlap(y[i], r * c * element_size(dtype), data[i], r * mx::data_stride(c)))
-      return host::set_error(MUON_ERR_ARG, "matrix %d: y must not overlap data", i);
+    spans.push_back(reads(data[i], r * mx::data_stride(c), "data"));
+    spans.push_back(reads(scales[i], scale_bytes(r, c), "scales"));
+    spans.push_back(writes(y[i], r * c * element_size(dtype), "y"));
   }
+  TRY(check_apart(spans.data(), spans.size()));
   int sms = 0;
   TRY(host::device_sms(&sms));
   cudaStream_t s = as_stream(stream);
@@ -310,8 +362,10 @@ int product_impl(long long m, long long n, long long k, const void* a_data, cons
   TRY(check_pointer(a_scales, 16, "a_scales"));
   TRY(check_pointer(b_data, 16, "b_data"));
   TRY(check_pointer(b_scales, 16, "b_scales"));
-  if (overlap(out, ob, a_data, m * mx::data_stride(k)) || overlap(out, ob, b_data, n * mx::data_stride(k)))
-    return host::set_error(MUON_ERR_ARG, "out must not overlap an operand");
+  Span spans[] = {writes(out, ob, "out"), reads(a_data, m * mx::data_stride(k), "a_data"),
+                  reads(a_scales, scale_bytes(m, k), "a_scales"), reads(b_data, n * mx::data_stride(k), "b_data"),
+                  reads(b_scales, scale_bytes(n, k), "b_scales")};
+  TRY(check_apart(spans, std::size(spans)));
   TRY(host::device_sms(&sms));
   mx::ProductParams p{};
   TRY(host::workspace_status(s, &p.status));
