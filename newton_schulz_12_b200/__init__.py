@@ -248,7 +248,10 @@ class MuonStepPlan(_Replayable):
     muon_step_ex (options as there; a schedule fixes the step count).  With
     ``mx_forms`` every call ends by writing the new weights' 4-bit forms, for
     the layer's forward and backward products: ``plan.mx_forms[i]`` is the pair
-    (rows, columns) of ``params[i]``, filled at construction, too.
+    (rows, columns) of ``params[i]``, filled at construction, too, on the stream
+    that is current then.  A call or a replay on another stream comes after that
+    filling by itself; whoever reads the forms on another stream than the last
+    call's orders that, as for the weights.
     """
 
     def __init__(self, params, grads, momentum_bufs, beta=0.95, nesterov=True, lr=0.05, wd=0.0,
@@ -297,6 +300,8 @@ class MuonStepPlan(_Replayable):
         self.mx_forms, self._quantize = None, None
         if mx_forms:
             self.mx_forms = muon_mx_quantize(self.params, rows=True, cols=True)
+            filled_on = torch.cuda.current_stream(self.params[0].device)
+            self._filled, self._used_on = filled_on.record_event(), {filled_on.cuda_stream}
             pairs = [(r._pointers(), c._pointers()) for r, c in self.mx_forms]
             self._quantize = layers._marshal_quantize(self.params, [(*s, s[1]) for s in shapes],
                                                       [r for r, _ in pairs], [c for _, c in pairs])
@@ -311,7 +316,34 @@ class MuonStepPlan(_Replayable):
                        float(old[2] if lr is None else lr), float(old[3] if wd is None else wd),
                        int(old[4] if steps is None else steps))
 
+    def _order(self, stream):
+        """Before the first use of the forms on ``stream``: it waits for their filling, and their memory
+        is not given away before what runs on it is done."""
+        raw = _stream(stream).value or 0
+        if raw in self._used_on:
+            return
+        device = self.params[0].device
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(raw, device=device)
+        for pair in self.mx_forms:
+            for form in pair:
+                for t in form._tensors():
+                    t.record_stream(stream)
+        with torch.cuda.stream(stream):
+            if torch.cuda.is_current_stream_capturing():
+                return  # it may not wait for what was not captured: the replays' streams do
+        stream.wait_event(self._filled)
+        self._used_on.add(raw)
+
+    def replay(self):
+        """One step by replaying the graph recorded by ``capture`` (on the current stream)."""
+        if self._quantize is not None:
+            self._order(None)
+        super().replay()
+
     def __call__(self, stream=None):
+        if self._quantize is not None:
+            self._order(stream)
         beta, nest, lr, wd, steps = self._hyper
         if self._fn_ex is not None:
             flags, beta2 = self._ex
