@@ -298,7 +298,9 @@ class MuonStepPlan(_Replayable):
         if self._table is not None or self._state is not None or cautious_wd:
             self._fn_ex = _lib.lib().muon_step_ex
         self.mx_forms, self._quantize = None, None
-        if mx_forms:
+        if mx_forms and not self.params:
+            self.mx_forms = []
+        elif mx_forms:
             self.mx_forms = muon_mx_quantize(self.params, rows=True, cols=True)
             filled_on = torch.cuda.current_stream(self.params[0].device)
             self._filled, self._used_on = filled_on.record_event(), {filled_on.cuda_stream}
