@@ -384,6 +384,9 @@ def muon_mx_quantize(x, rows=True, cols=False, out=None, stream=None):
         given = [out] if single else list(out)
         if len(given) != len(xs):
             raise ValueError("one out for each matrix is required")
+        for i, g in enumerate(given):
+            if rows and cols and not isinstance(g, (tuple, list)):
+                raise ValueError(f"out[{i}] must be the pair (row form, column form)")
         given = [tuple(g) if rows and cols else (g,) for g in given]
         for i, (g, (r, c, _)) in enumerate(zip(given, sizes)):
             want = ([(r, c)] if rows else []) + ([(c, r)] if cols else [])
