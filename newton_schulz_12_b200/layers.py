@@ -3,7 +3,9 @@ gradient, and 4-bit microscaled (MX) quantisation with the layer's products.
 
 Argument marshalling over the C ABI (include/muon.h), like the rest of the
 binding.  Calls run on the tensors' device, on ``stream`` or that device's
-current stream, and allocate their results and scratch there.
+current stream, and allocate their results and scratch there.  Like the rest of
+the binding they are not recorded by autograd: results never require a
+gradient, whatever the inputs do, and the gradients are calls of their own.
 """
 from __future__ import annotations
 
