@@ -333,7 +333,7 @@ class MuonStepPlan(_Replayable):
                     t.record_stream(stream)
         with torch.cuda.stream(stream):
             if torch.cuda.is_current_stream_capturing():
-                return  # it may not wait for what was not captured: the replays' streams do
+                return  # it may not wait for what was not captured; whoever replays the graph orders that
         stream.wait_event(self._filled)
         self._used_on.add(raw)
 
